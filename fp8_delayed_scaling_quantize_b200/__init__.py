@@ -27,6 +27,7 @@ FP8_RING_HISTORY = 16
 FP8_RING_BYTES = 80
 FP8_IN_BF16, FP8_IN_F16, FP8_IN_F32 = 0, 1, 2
 FP8_QL_ROW, FP8_QL_COL, FP8_QL_BOTH = 0, 1, 2
+FP8_ACT_NONE, FP8_ACT_RELU, FP8_ACT_GELU, FP8_ACT_GELU_TANH, FP8_ACT_SILU = 0, 1, 2, 3, 4
 FP8_QUANTIZE_SEED_RING = 1
 FP8_QUANTIZE_DEFER_FOLD = 2
 
@@ -101,6 +102,9 @@ def _load():
         "fp8_mm_splitk_static": (I, [P, I, P, I, P, P, I, I64, I64, I64, I64, I64, I64, I64, P, P, I, P,
                                      ctypes.c_int32, P]),
         "fp8_mm_grouped": (I, [P, ctypes.c_int32, P]),
+        "fp8_mm_act": (I, [P, I, P, I, P, P, I, I64, I64, I64, I64, I64, I64, I64, P, P, I, I, P, I64, P, P, P]),
+        "fp8_mm_act_out8": (I, [P, I, P, I, P, P, I, I64, I64, I64, I64, I64, I64, I64, P, P, I, I, P, I, P, P, P, P,
+                                P]),
     }
     for name, (res, args) in sig.items():
         try:
@@ -234,6 +238,23 @@ def fp8_mm_out8(a8, fa, b8, fb, sa, sb, layout, M, N, K, batch, stride_a, stride
                                   int(M), int(N), int(K), int(batch), int(stride_a), int(stride_b), int(stride_c),
                                   _ptr(bias), _ptr(bias_scale), int(bias_fmt), int(out_fmt), _ptr(out_ring),
                                   _ptr(out8), _ptr(out_amax), _ptr(out_scale), _stream(stream)), "fp8_mm_out8")
+
+
+def fp8_mm_act(a8, fa, b8, fb, sa, sb, layout, M, N, K, batch, stride_a, stride_b, stride_c, bias, bias_scale,
+               bias_fmt, act, residual, stride_r, preact, out, stream=None):
+    return _check(lib.fp8_mm_act(_ptr(a8), int(fa), _ptr(b8), int(fb), _ptr(sa), _ptr(sb), int(layout), int(M), int(N),
+                                 int(K), int(batch), int(stride_a), int(stride_b), int(stride_c), _ptr(bias),
+                                 _ptr(bias_scale), int(bias_fmt), int(act), _ptr(residual), int(stride_r),
+                                 _ptr(preact), _ptr(out), _stream(stream)), "fp8_mm_act")
+
+
+def fp8_mm_act_out8(a8, fa, b8, fb, sa, sb, layout, M, N, K, batch, stride_a, stride_b, stride_c, bias, bias_scale,
+                    bias_fmt, act, preact, out_fmt, out_ring, out8, out_amax, out_scale, stream=None):
+    return _check(lib.fp8_mm_act_out8(_ptr(a8), int(fa), _ptr(b8), int(fb), _ptr(sa), _ptr(sb), int(layout), int(M),
+                                      int(N), int(K), int(batch), int(stride_a), int(stride_b), int(stride_c),
+                                      _ptr(bias), _ptr(bias_scale), int(bias_fmt), int(act), _ptr(preact),
+                                      int(out_fmt), _ptr(out_ring), _ptr(out8), _ptr(out_amax), _ptr(out_scale),
+                                      _stream(stream)), "fp8_mm_act_out8")
 
 
 def fp8_mm_grouped(problems, stream=None):

@@ -14,7 +14,7 @@ PKG = os.path.dirname(os.path.abspath(__file__))
 ROOT = os.path.dirname(PKG)
 CSRC = os.path.join(PKG, "csrc")
 LIB = os.path.join(PKG, "libfp8lite.so")
-SOURCES = ("quantize.cu", "gemm.cu", "colsum.cu")
+SOURCES = ("quantize.cu", "gemm.cu", "gemm_act.cu", "colsum.cu")
 
 
 NVCC_FLAGS = [
@@ -46,15 +46,19 @@ def build(force: bool = False, verbose: bool = False, extra=()) -> str:
     """Compile the library if any source is newer than it. Returns its path."""
     if not force and not stale():
         return LIB
-    objs = []
-    for src in SOURCES:
+    objs, running = [], []
+    for src in SOURCES:  # one compiler per source, side by side
         obj = os.path.join(CSRC, src.replace(".cu", ".o"))
         cmd = [_nvcc(), *NVCC_FLAGS, *extra, "-I", os.path.join(ROOT, "include"), "-I", CSRC,
                "-c", os.path.join(CSRC, src), "-o", obj]
         if verbose:
             print(" ".join(cmd), flush=True)
-        subprocess.run(cmd, check=True)
+        running.append((cmd, subprocess.Popen(cmd)))
         objs.append(obj)
+    done = [(cmd, p.wait()) for cmd, p in running]  # every compiler ends before an error is raised
+    for cmd, rc in done:
+        if rc:
+            raise subprocess.CalledProcessError(rc, cmd)
     link = [_nvcc(), "-gencode", "arch=compute_100a,code=sm_100a", "-shared", "-cudart", "static",
             "-Xcompiler", "-fPIC", *objs, "-o", LIB]
     if verbose:

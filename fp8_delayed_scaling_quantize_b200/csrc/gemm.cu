@@ -3,6 +3,7 @@
 // split-K and grouped launches, and the device error word.
 
 #include "gemm_kernel.cuh"
+#include "errors.h"
 
 using namespace fp8lite;
 
@@ -39,31 +40,12 @@ fp8_status mm_impl(const uint8_t* a8, fp8_fmt fa, const uint8_t* b8, fp8_fmt fb,
                    void* stream) {
     if (split_k < 0 || split_k > kMaxSplit) return FP8_ERR_INVALID_ARG;
     if (workspace && !aligned(workspace, 16)) return FP8_ERR_ALIGNMENT;
-    if (!valid_fmt(fa) || !valid_fmt(fb)) return FP8_ERR_INVALID_ARG;
-    if (layout != FP8_NT && layout != FP8_NN && layout != FP8_TN) return FP8_ERR_INVALID_ARG;
-    if (!a8 || !b8 || !sa || !sb || !out) return FP8_ERR_INVALID_ARG;
-    if (M < 1 || N < 1 || K < 1 || batch < 1) return FP8_ERR_INVALID_ARG;
-    if (stride_a < 0 || stride_b < 0 || stride_c < 0) return FP8_ERR_INVALID_ARG;
-    if (bias_scale && !bias) return FP8_ERR_INVALID_ARG;
-    if (bias && bias_scale && !valid_fmt(bias_fmt)) return FP8_ERR_INVALID_ARG;
     if (o8.on && (!valid_fmt(o8.fmt) || !o8.ring || !o8.scale)) return FP8_ERR_INVALID_ARG;
-    if (M >= (int64_t(1) << 31) || N >= (int64_t(1) << 31) || K >= (int64_t(1) << 31) ||
-        batch >= (int64_t(1) << 31))
-        return FP8_ERR_UNSUPPORTED;
-    if (batch > 1 && stride_c < M * N) return FP8_ERR_INVALID_ARG;
-    const int64_t tiles = ((M + BM - 1) / BM) * ((N + 63) / 64) * batch;
-    if (tiles >= (int64_t(1) << 31)) return FP8_ERR_UNSUPPORTED;
-
+    const fp8_status st0 = check_mm(a8, fa, b8, fb, sa, sb, layout, M, N, K, batch, stride_a, stride_b, stride_c, bias,
+                                    bias_scale, bias_fmt, out, o8.on ? 1 : 4);
+    if (st0 != FP8_OK) return st0;
     const bool a_mn = layout == FP8_TN;
     const bool b_mn = layout != FP8_NT;
-    // contiguous extent of each operand = TMA row pitch in bytes
-    const int64_t a_pitch = a_mn ? M : K;
-    const int64_t b_pitch = b_mn ? N : K;
-    if (a_pitch % 16 != 0 || b_pitch % 16 != 0) return FP8_ERR_ALIGNMENT;
-    if (!aligned(a8, 16) || !aligned(b8, 16)) return FP8_ERR_ALIGNMENT;
-    if (stride_a % 16 != 0 || stride_b % 16 != 0) return FP8_ERR_ALIGNMENT;
-    if (!aligned(out, o8.on ? 1 : 4) || !aligned(sa, 4) || !aligned(sb, 4)) return FP8_ERR_ALIGNMENT;
-    if (bias && !bias_scale && !aligned(bias, 2)) return FP8_ERR_ALIGNMENT;
     if (o8.on && (!aligned(o8.ring, 4) || !aligned(o8.scale, 4) || !aligned(o8.amax, 4))) return FP8_ERR_ALIGNMENT;
     if (batch == 1) { stride_a = 0; stride_b = 0; }
 
@@ -167,7 +149,7 @@ fp8_status launch_group(const GroupTab<true>& g, int total_units, cudaStream_t s
     p.sb = g.q[0].sb;
     const int units = total_units < sm_count() ? total_units : sm_count();
     const CUtensorMap none = {};
-    return launch_pdl(kern, units, kThreads, L::kAlloc, st, 1, none, none, none, p, g);
+    return launch_pdl(kern, units, kThreads, L::kAlloc, st, 1, none, none, none, p, g, EpArgs<false>{});
 }
 
 // Tile width of a grouped launch: the persistent grid hands out the units in
@@ -443,9 +425,9 @@ extern "C" fp8_status fp8_mm_splitk_static(const uint8_t* a8, fp8_fmt fa, const 
 
 extern "C" fp8_status fp8_last_device_error(void) {
     if (cudaDeviceSynchronize() != cudaSuccess) return FP8_ERR_CUDA;
-    uint32_t v = 0;
-    if (!take_error_word(&v)) return FP8_ERR_CUDA;
-    return v ? FP8_ERR_DEVICE_TIMEOUT : FP8_OK;
+    uint32_t v = 0, w = 0;
+    if (!take_error_word(&v) || !gemm_act_error(&w)) return FP8_ERR_CUDA;
+    return (v | w) ? FP8_ERR_DEVICE_TIMEOUT : FP8_OK;
 }
 
 extern "C" fp8_status fp8_selftest_wait_timeout(uint32_t limit_us, void* stream) {

@@ -54,6 +54,7 @@
 #include <algorithm>
 #include <mutex>
 
+#include "act.cuh"
 #include "common.cuh"
 #include "sm100.cuh"
 
@@ -129,6 +130,20 @@ template <>
 struct GroupTab<true> {
     GroupProblem q[kMaxEntries];
     int count;
+};
+
+// Activation epilogue (fp8_mm_act, fp8_mm_act_out8): the activation, the bf16
+// residual added after it, and where z (the activation's input) is kept.
+template <bool EP>
+struct EpArgs {};  // other launches carry none of it
+template <>
+struct EpArgs<true> {
+    CUtensorMap tz;            // store map of preact (fast launches)
+    int act;
+    int fast;                  // whole tiles: every pointer, stride and N aligned for 16-byte accesses
+    const uint16_t* residual;  // may be the output itself
+    int64_t stride_r;
+    uint16_t* preact;          // laid out as the output
 };
 
 // The i-th work unit of a CTA whose first unit is unit0, the persistent grid
@@ -245,9 +260,18 @@ __device__ __forceinline__ uint32_t pack_bf16x2(float lo, float hi) {
     return r;
 }
 
+__device__ __forceinline__ uint16_t bf16_bits(float v) {
+    uint16_t h;
+    asm("cvt.rn.bf16.f32 %0, %1;" : "=h"(h) : "f"(v));
+    return h;
+}
+
+__device__ __forceinline__ float bf16_value(uint16_t h) { return __uint_as_float(uint32_t(h) << 16); }
+
 // Shared-memory plan of one CTA. CTAS = 2: an MMA pair, each CTA holding its
 // 128 rows of A and BN/2 columns of B per stage.
-template <int BN, int STAGES, int CTAS>
+// STG: staging tiles of the epilogue.
+template <int BN, int STAGES, int CTAS, int STG = 3>
 struct Smem {
     static constexpr int kABytes = BM * BK;
     static constexpr int kBBytes = (BN / CTAS) * BK;
@@ -256,8 +280,11 @@ struct Smem {
     // three 128-row x 32-column bf16 staging tiles (64-byte swizzle), used in
     // turn, so that a chunk waits only for the store two chunks back; 24 KB
     // in all, so that a waiting kernel's small blocks still fit on the SM
-    // beside this CTA
-    static constexpr int kStgBufs = 3;
+    // beside this CTA. An activation epilogue takes four: its residual is
+    // written into the tile after the next, which must be free as early
+    static constexpr int kStgBufs = STG;
+    static constexpr int kStgPending = 1;  // stores that may still be reading their tile when one more is issued
+    static_assert(STG >= 3, "");
     static constexpr int kStgBytes = BM * 32 * 2;
     static constexpr int kStgOffset = STAGES * kStageBytes;  // a multiple of 1024
     static constexpr int kBiasOffset = kStgOffset + kStgBufs * kStgBytes;  // BN fp32 bias values
@@ -341,11 +368,136 @@ __device__ __forceinline__ void stage_and_store(uint32_t stg0, int n_st, int row
     // the store two blocks back has read its tile, which the next block
     // reuses (only the newest store may still be reading); the barrier
     // publishes that and this block
-    if (store_lead) bulk_wait_read<L::kStgBufs - 2>();
+    if (store_lead) bulk_wait_read<L::kStgPending>();
     epilogue_bar();
     if (store_lead) {
         tma_store_3d(map_c, stg, col0, m0, b);
         bulk_commit();
+    }
+}
+
+// The epilogue of one 128 x BN tile through an activation (unswapped tiles).
+// Per 32 columns: z = acc * inv + bias, kept as bf16 if asked for, then
+// act(z) + residual as bf16, or act(z) as FP8 codes under the output ring's
+// scale. A fast launch stages every bf16 block for a TMA store; its residual
+// arrives as 64-byte row pieces (a warp's load covers 8 rows), one block
+// ahead, and passes through the staging tile that the output block will take,
+// so that each thread finds its own row there. Only this warp's rows are
+// exchanged, and the thread that reads a row is the one that overwrites it.
+template <int BN, bool OUT8, typename L>
+__device__ __forceinline__ void epilogue_act(const GemmParams& p, const EpArgs<true>& ep, const CUtensorMap* map_c,
+                                             uint32_t t_row, const float* s_bias, uint32_t stg0, int& n_st, int q,
+                                             int lane, bool store_lead, float inv, float s_out, float& m_out, int m0,
+                                             int col_first, int b, int M, int N, bool vec_store) {
+    const int row_in_tile = q * 32 + lane;
+    const int row = m0 + row_in_tile;
+    const int left = (N - col_first + 31) / 32;
+    const int nch = left < BN / 32 ? left : BN / 32;
+    const bool has_z = ep.preact != nullptr, has_r = !OUT8 && ep.residual != nullptr;
+    const int64_t at = int64_t(b) * p.stride_c + int64_t(row) * N;  // this row in out and preact
+    const uint16_t* res = has_r ? ep.residual + int64_t(b) * ep.stride_r : nullptr;
+    const int piece = lane & 3, prow = q * 32 + (lane >> 2);  // residual pieces: rows prow + 8 j
+    uint4 rp[4];
+    auto load_residual = [&](int c) {
+        const int col = col_first + c * 32 + piece * 8;
+#pragma unroll
+        for (int j = 0; j < 4; ++j) {
+            const int r = m0 + prow + 8 * j;
+            rp[j] = (r < M && col < N) ? __ldcg(reinterpret_cast<const uint4*>(res + int64_t(r) * N + col))
+                                       : make_uint4(0, 0, 0, 0);
+        }
+    };
+    auto process = [&](const uint32_t (&acc)[32], int c) {
+        const int col0 = col_first + c * 32;
+        float y[32];
+#pragma unroll
+        for (int i = 0; i < 32; ++i) y[i] = fmaf(__uint_as_float(acc[i]), inv, s_bias[c * 32 + i]);
+        if (ep.fast) {
+            if (has_r) {
+                const uint32_t stg = stg0 + uint32_t((n_st + has_z) % L::kStgBufs) * L::kStgBytes;
+#pragma unroll
+                for (int j = 0; j < 4; ++j) {
+                    const int r = prow + 8 * j;
+                    asm volatile("st.shared.v4.b32 [%0], {%1, %2, %3, %4};" ::"r"(stg + r * 64 +
+                                                                                  ((piece ^ ((r >> 1) & 3)) << 4)),
+                                 "r"(rp[j].x), "r"(rp[j].y), "r"(rp[j].z), "r"(rp[j].w)
+                                 : "memory");
+                }
+                __syncwarp();
+                if (c + 1 < nch) load_residual(c + 1);
+            }
+            if (has_z) {
+                stage_and_store<L>(stg0, n_st, row_in_tile, y, store_lead, &ep.tz, col0, m0, b);
+                ++n_st;
+            }
+            act_apply(ep.act, y);
+            if (has_r) {
+                const uint32_t stg = stg0 + uint32_t(n_st % L::kStgBufs) * L::kStgBytes;
+#pragma unroll
+                for (int j = 0; j < 4; ++j) {
+                    uint32_t w[4];
+                    asm volatile("ld.shared.v4.b32 {%0, %1, %2, %3}, [%4];"
+                                 : "=r"(w[0]), "=r"(w[1]), "=r"(w[2]), "=r"(w[3])
+                                 : "r"(stg + row_in_tile * 64 + ((j ^ ((row_in_tile >> 1) & 3)) << 4))
+                                 : "memory");
+#pragma unroll
+                    for (int k = 0; k < 4; ++k) {
+                        y[8 * j + 2 * k] += __uint_as_float(w[k] << 16);
+                        y[8 * j + 2 * k + 1] += __uint_as_float(w[k] & 0xFFFF0000u);
+                    }
+                }
+            }
+        } else {
+            if (has_z && row < M) {
+#pragma unroll
+                for (int i = 0; i < 32; ++i)
+                    if (col0 + i < N) ep.preact[at + col0 + i] = bf16_bits(y[i]);
+            }
+            act_apply(ep.act, y);
+            if (has_r && row < M) {
+#pragma unroll
+                for (int i = 0; i < 32; ++i)
+                    if (col0 + i < N) y[i] += bf16_value(res[int64_t(row) * N + col0 + i]);
+            }
+        }
+        if constexpr (OUT8) {
+            if (row < M) {
+                uint32_t w[8];
+#pragma unroll
+                for (int j = 0; j < 8; ++j) {
+#pragma unroll
+                    for (int k = 0; k < 4; ++k)
+                        if (col0 + 4 * j + k < N) m_out = fmaxf(m_out, fabsf(y[4 * j + k]));
+                    w[j] = cvt_fp8x2(p.out_fmt, __fmul_rn(y[4 * j], s_out), __fmul_rn(y[4 * j + 1], s_out)) |
+                           (cvt_fp8x2(p.out_fmt, __fmul_rn(y[4 * j + 2], s_out), __fmul_rn(y[4 * j + 3], s_out)) << 16);
+                }
+                uint8_t* dst = reinterpret_cast<uint8_t*>(p.out) + at + col0;
+                if (vec_store && col0 + 32 <= N) {
+                    reinterpret_cast<uint4*>(dst)[0] = make_uint4(w[0], w[1], w[2], w[3]);
+                    reinterpret_cast<uint4*>(dst)[1] = make_uint4(w[4], w[5], w[6], w[7]);
+                } else {
+#pragma unroll
+                    for (int i = 0; i < 32; ++i)
+                        if (col0 + i < N) dst[i] = uint8_t(w[i >> 2] >> (8 * (i & 3)));
+                }
+            }
+        } else if (ep.fast) {
+            stage_and_store<L>(stg0, n_st, row_in_tile, y, store_lead, map_c, col0, m0, b);
+            ++n_st;
+        } else if (row < M) {
+#pragma unroll
+            for (int i = 0; i < 32; ++i)
+                if (col0 + i < N) p.out[at + col0 + i] = bf16_bits(y[i]);
+        }
+    };
+    if (ep.fast && has_r) load_residual(0);
+#pragma unroll 1
+    for (int c = 0; c < nch; ++c) {
+        uint32_t r[32];
+        __syncwarp();
+        tmem_ld<32>(t_row + c * 32, r);
+        tmem_ld_wait();
+        process(r, c);
     }
 }
 
@@ -364,12 +516,13 @@ __device__ __forceinline__ void stage_and_store(uint32_t stg0, int n_st, int row
 // column, scales, bias and output come from the entry of each unit, A_MN /
 // B_MN only give the defaults and BN is the widest tile.
 template <int BN, bool A_MN, bool B_MN, int STAGES, bool HAS_BIAS, int CTAS, bool SPLIT, bool SWAP, bool OUT8,
-          bool GROUP = false>
+          bool GROUP = false, bool EP = false>
 __global__ void __maxnreg__(168)
 fp8_gemm_kernel(const __grid_constant__ CUtensorMap tm_a, const __grid_constant__ CUtensorMap tm_b,
                 const __grid_constant__ CUtensorMap tm_c, const GemmParams p,
-                const __grid_constant__ GroupTab<GROUP> grp) {
-    using L = Smem<BN, STAGES, CTAS>;
+                const __grid_constant__ GroupTab<GROUP> grp, const __grid_constant__ EpArgs<EP> ep) {
+    using L = Smem<BN, STAGES, CTAS, EP ? 4 : 3>;
+    static_assert(!EP || (HAS_BIAS && !GROUP), "an activation epilogue always has its bias slots");
     static_assert(!(B_MN && CTAS == 2 && BN != 256), "MN-major B halves must be whole 128-byte atoms");
     static_assert(!GROUP || (CTAS == 1 && !SPLIT && !SWAP && !OUT8), "grouped launches use plain one-SM tiles");
     extern __shared__ __align__(1024) uint8_t smem_raw[];
@@ -426,6 +579,9 @@ fp8_gemm_kernel(const __grid_constant__ CUtensorMap tm_a, const __grid_constant_
             tma_prefetch(&tm_a);
             tma_prefetch(&tm_b);
             if (tma_store) tma_prefetch(&tm_c);
+            if constexpr (EP) {
+                if (ep.fast && ep.preact) tma_prefetch(&ep.tz);
+            }
         }
     }
     if (warp == 1) {
@@ -754,7 +910,7 @@ fp8_gemm_kernel(const __grid_constant__ CUtensorMap tm_a, const __grid_constant_
             // swapped operands: this thread's TMEM lane is output column `row`
             // of C (the kernel's M is C's N), its accumulator columns are C's rows
             float bias_row = 0.0f;
-            if (SWAP && HAS_BIAS && row < M) {
+            if (SWAP && HAS_BIAS && row < M && (!EP || bias_kind != 0)) {
                 if (bias_kind == 1)
                     bias_row = __uint_as_float(uint32_t(__ldg(static_cast<const uint16_t*>(bias_ptr) + row)) << 16);
                 else
@@ -763,7 +919,11 @@ fp8_gemm_kernel(const __grid_constant__ CUtensorMap tm_a, const __grid_constant_
             }
             uint16_t* orow = SWAP ? out_base + int64_t(b) * p.stride_c + row
                                   : out_base + int64_t(b) * p.stride_c + int64_t(row) * N;
-            if constexpr (!SPLIT && !SWAP && !OUT8) {
+            if constexpr (EP && !SWAP) {
+                epilogue_act<BN, OUT8, L>(p, ep, &tm_c, t_row, s_bias, stg0, n_st, q, lane, store_lead, inv, s_out, m_out,
+                                          m0, nb * BN, b, M, N, vec_store);
+            }
+            if constexpr (!EP && !SPLIT && !SWAP && !OUT8) {
                 if (tma_store) {
                     // The common case, pipelined: chunk c + 1's accumulator
                     // columns leave TMEM while chunk c is converted, staged and
@@ -803,8 +963,10 @@ fp8_gemm_kernel(const __grid_constant__ CUtensorMap tm_a, const __grid_constant_
                     continue;
                 }
             }
+            // an activation epilogue is done here; a swapped one is part of the loop
+            const int n_chunks = EP && !SWAP ? 0 : ebn / CW;
 #pragma unroll 1
-            for (int c = 0; c < ebn / CW; ++c) {
+            for (int c = 0; c < n_chunks; ++c) {
                 const int col0 = n_base + nb * ebn + c * CW;
                 if (col0 >= N) break;  // uniform over the epilogue warps
                 uint32_t r[CW];
@@ -853,7 +1015,30 @@ fp8_gemm_kernel(const __grid_constant__ CUtensorMap tm_a, const __grid_constant_
                 if constexpr (SWAP) {
                     // C[col0 + i][row]: lanes hold consecutive columns, so each
                     // store instruction of a warp writes 64 contiguous bytes
-                    if (row < M) {
+                    if constexpr (EP) {
+                        // the same, through the activation: z to preact, act(z) + residual to out
+                        float y[CW];
+#pragma unroll
+                        for (int i = 0; i < CW; ++i) y[i] = fmaf(__uint_as_float(r[i]), inv, bias_row);
+                        if (row < M) {
+                            if (ep.preact) {
+                                uint16_t* z = ep.preact + (orow - out_base);
+#pragma unroll
+                                for (int i = 0; i < CW; ++i)
+                                    if (col0 + i < N) z[int64_t(col0 + i) * M] = bf16_bits(y[i]);
+                            }
+                            act_apply(ep.act, y);
+                            if (ep.residual) {
+                                const uint16_t* res = ep.residual + int64_t(b) * ep.stride_r + row;
+#pragma unroll
+                                for (int i = 0; i < CW; ++i)
+                                    if (col0 + i < N) y[i] += bf16_value(res[int64_t(col0 + i) * M]);
+                            }
+#pragma unroll
+                            for (int i = 0; i < CW; ++i)
+                                if (col0 + i < N) orow[int64_t(col0 + i) * M] = bf16_bits(y[i]);
+                        }
+                    } else if (row < M) {
 #pragma unroll
                         for (int i = 0; i < CW; ++i) {
                             if (col0 + i >= N) break;
@@ -916,7 +1101,7 @@ fp8_gemm_kernel(const __grid_constant__ CUtensorMap tm_a, const __grid_constant_
                         // the store two blocks back has read its tile, which the next
                         // block reuses (only the newest store may still be reading);
                         // the barrier publishes that and this block
-                        if (store_lead) bulk_wait_read<L::kStgBufs - 2>();
+                        if (store_lead) bulk_wait_read<L::kStgPending>();
                         epilogue_bar();
                         if (store_lead) {
                             tma_store_3d(map_c, stg, col0, m0, b);
@@ -954,7 +1139,7 @@ fp8_gemm_kernel(const __grid_constant__ CUtensorMap tm_a, const __grid_constant_
         // the staging tiles must outlive the stores that read them; the global
         // writes themselves complete with the grid (a dependent kernel's
         // griddepcontrol.wait and stream order both see them)
-        if ((GROUP || tma_store) && store_lead) bulk_wait_read<0>();
+        if ((GROUP || EP || tma_store) && store_lead) bulk_wait_read<0>();
         if constexpr (OUT8) {
             // the CTA's amax of the output: one atomicMax, then a ticket; the
             // CTA holding the last ticket folds it into the output's ring
@@ -1074,11 +1259,12 @@ struct HostArgs {
     int64_t batch, stride_b;
 };
 
-template <int BN, bool A_MN, bool B_MN, int STAGES, bool HAS_BIAS, int CTAS, bool SPLIT, bool SWAP, bool OUT8>
+template <int BN, bool A_MN, bool B_MN, int STAGES, bool HAS_BIAS, int CTAS, bool SPLIT, bool SWAP, bool OUT8,
+          bool EP = false>
 fp8_status launch_one(const CUtensorMap& ta, const CUtensorMap& tb, const CUtensorMap& tc, GemmParams p,
-                      const HostArgs& h, cudaStream_t st) {
-    using L = Smem<BN, STAGES, CTAS>;
-    auto kern = fp8_gemm_kernel<BN, A_MN, B_MN, STAGES, HAS_BIAS, CTAS, SPLIT, SWAP, OUT8>;
+                      const HostArgs& h, cudaStream_t st, const EpArgs<EP>& ep = {}) {
+    using L = Smem<BN, STAGES, CTAS, EP ? 4 : 3>;
+    auto kern = fp8_gemm_kernel<BN, A_MN, B_MN, STAGES, HAS_BIAS, CTAS, SPLIT, SWAP, OUT8, false, EP>;
     static bool attr_set[64] = {false};
     int dev = 0;
     if (cudaGetDevice(&dev) != cudaSuccess || dev < 0 || dev >= 64) return FP8_ERR_CUDA;
@@ -1101,14 +1287,21 @@ fp8_status launch_one(const CUtensorMap& ta, const CUtensorMap& tb, const CUtens
     // a cluster split runs each tile's splits as one cluster (every unit in
     // the grid's one round, so the grid is a whole number of clusters)
     const int cluster = p.csplit ? p.split : CTAS;
-    return launch_pdl(kern, units * CTAS, kThreads, L::kAlloc, st, cluster, ta, tb, tc, p, GroupTab<false>{});
+    return launch_pdl(kern, units * CTAS, kThreads, L::kAlloc, st, cluster, ta, tb, tc, p, GroupTab<false>{}, ep);
 }
 
-template <int BN, bool A_MN, bool B_MN, int STAGES, int CTAS, bool SWAP = false, bool OUT8 = false>
-fp8_status launch(const CUtensorMap& ta, const CUtensorMap& tb, GemmParams p, const HostArgs& h, cudaStream_t st) {
+template <int BN, bool A_MN, bool B_MN, int STAGES, int CTAS, bool SWAP = false, bool OUT8 = false, bool EP = false>
+fp8_status launch(const CUtensorMap& ta, const CUtensorMap& tb, GemmParams p, const HostArgs& h, cudaStream_t st,
+                  const EpArgs<EP>& ep = {}) {
     CUtensorMap tc = {};
     if (p.tma_store && !make_out_map(&tc, p.out, p.N, p.M, h.batch, uint64_t(p.stride_c) * 2)) return FP8_ERR_CUDA;
-    if constexpr (OUT8) {  // no split, no swap
+    if constexpr (EP) {  // always with bias slots; only a swapped problem splits (as a cluster)
+        if constexpr (SWAP) {
+            if (p.split > 1)
+                return launch_one<BN, A_MN, B_MN, STAGES, true, CTAS, true, SWAP, false, true>(ta, tb, tc, p, h, st, ep);
+        }
+        return launch_one<BN, A_MN, B_MN, STAGES, true, CTAS, false, SWAP, OUT8, true>(ta, tb, tc, p, h, st, ep);
+    } else if constexpr (OUT8) {  // no split, no swap
         return p.bias_kind ? launch_one<BN, A_MN, B_MN, STAGES, true, CTAS, false, false, true>(ta, tb, tc, p, h, st)
                            : launch_one<BN, A_MN, B_MN, STAGES, false, CTAS, false, false, true>(ta, tb, tc, p, h, st);
     } else {
@@ -1203,9 +1396,9 @@ inline TileChoice choose_tile(int64_t M, int64_t N, int64_t K, int64_t batch, bo
     return best;
 }
 
-template <bool A_MN, bool B_MN, bool OUT8 = false>
+template <bool A_MN, bool B_MN, bool OUT8 = false, bool EP = false>
 fp8_status dispatch(const CUtensorMap& ta, GemmParams p, const HostArgs& h, void* ws, size_t ws_bytes,
-                    int split_req, cudaStream_t st) {
+                    int split_req, cudaStream_t st, const EpArgs<EP>& ep = {}) {
     const TileChoice tc = choose_tile(p.M, p.N, p.K, h.batch, B_MN, sm_count(), split_req);
     if (tc.split == 0) return FP8_ERR_UNSUPPORTED;
     const bool pair = tc.pair;
@@ -1223,10 +1416,10 @@ fp8_status dispatch(const CUtensorMap& ta, GemmParams p, const HostArgs& h, void
     const bool ok = B_MN ? make_map(&tb, h.b8, p.N, p.K, h.batch, sb_bytes, 128, BK)
                          : make_map(&tb, h.b8, p.K, p.N, h.batch, sb_bytes, BK, b_box_n);
     if (!ok) return FP8_ERR_CUDA;
-    if (pair) return launch<256, A_MN, B_MN, 6, 2, false, OUT8>(ta, tb, p, h, st);
-    if (bn == 256) return launch<256, A_MN, B_MN, 4, 1, false, OUT8>(ta, tb, p, h, st);
-    if (bn == 128) return launch<128, A_MN, B_MN, 6, 1, false, OUT8>(ta, tb, p, h, st);
-    if constexpr (!B_MN) return launch<64, A_MN, B_MN, 8, 1, false, OUT8>(ta, tb, p, h, st);
+    if (pair) return launch<256, A_MN, B_MN, 6, 2, false, OUT8, EP>(ta, tb, p, h, st, ep);
+    if (bn == 256) return launch<256, A_MN, B_MN, 4, 1, false, OUT8, EP>(ta, tb, p, h, st, ep);
+    if (bn == 128) return launch<128, A_MN, B_MN, 6, 1, false, OUT8, EP>(ta, tb, p, h, st, ep);
+    if constexpr (!B_MN) return launch<64, A_MN, B_MN, 8, 1, false, OUT8, EP>(ta, tb, p, h, st, ep);
     return FP8_ERR_UNSUPPORTED;
 }
 
@@ -1269,10 +1462,10 @@ inline int swap_split(int64_t M, int64_t N, int64_t K, int64_t batch, int split_
     return best;
 }
 
-template <bool A_MN>
+template <bool A_MN, bool EP = false>
 fp8_status dispatch_swap(const uint8_t* a8, int fa, const uint8_t* b8, int fb, int64_t M, int64_t N, int64_t K,
                          int64_t batch, int64_t stride_a, int64_t stride_b, GemmParams p, void* ws, size_t ws_bytes,
-                         int split_req, cudaStream_t st) {
+                         int split_req, cudaStream_t st, const EpArgs<EP>& ep = {}) {
     const int bn = swap_bn(M);
     // The automatic choice without a workspace splits as a cluster: the
     // splits' partials go through split 0's staging area, which holds three
@@ -1312,8 +1505,36 @@ fp8_status dispatch_swap(const uint8_t* a8, int fa, const uint8_t* b8, int fb, i
     const bool ok_b = make_map(&tb, a8, K, M, batch, uint64_t(stride_a), BK, uint32_t(bn));
     if (!ok_a || !ok_b) return FP8_ERR_CUDA;
     const HostArgs h = {fb, fa, a8, batch, stride_a};
-    if (bn == 16) return launch<16, A_MN, false, 10, 1, true>(ta, tb, p, h, st);
-    return launch<32, A_MN, false, 9, 1, true>(ta, tb, p, h, st);
+    if (bn == 16) return launch<16, A_MN, false, 10, 1, true, false, EP>(ta, tb, p, h, st, ep);
+    return launch<32, A_MN, false, 9, 1, true, false, EP>(ta, tb, p, h, st, ep);
+}
+
+// The argument checks that every single-problem entry point shares. out_align:
+// bytes that the output must be aligned to.
+inline fp8_status check_mm(const void* a8, int fa, const void* b8, int fb, const float* sa, const float* sb, int layout,
+                           int64_t M, int64_t N, int64_t K, int64_t batch, int64_t stride_a, int64_t stride_b,
+                           int64_t stride_c, const void* bias, const float* bias_scale, int bias_fmt, const void* out,
+                           int out_align) {
+    if (!valid_fmt(fa) || !valid_fmt(fb)) return FP8_ERR_INVALID_ARG;
+    if (layout != FP8_NT && layout != FP8_NN && layout != FP8_TN) return FP8_ERR_INVALID_ARG;
+    if (!a8 || !b8 || !sa || !sb || !out) return FP8_ERR_INVALID_ARG;
+    if (M < 1 || N < 1 || K < 1 || batch < 1) return FP8_ERR_INVALID_ARG;
+    if (stride_a < 0 || stride_b < 0 || stride_c < 0) return FP8_ERR_INVALID_ARG;
+    if (bias_scale && !bias) return FP8_ERR_INVALID_ARG;
+    if (bias && bias_scale && !valid_fmt(bias_fmt)) return FP8_ERR_INVALID_ARG;
+    if (M >= (int64_t(1) << 31) || N >= (int64_t(1) << 31) || K >= (int64_t(1) << 31) ||
+        batch >= (int64_t(1) << 31))
+        return FP8_ERR_UNSUPPORTED;
+    if (batch > 1 && stride_c < M * N) return FP8_ERR_INVALID_ARG;
+    const int64_t tiles = ((M + BM - 1) / BM) * ((N + 63) / 64) * batch;
+    if (tiles >= (int64_t(1) << 31)) return FP8_ERR_UNSUPPORTED;
+    // contiguous extent of each operand = TMA row pitch in bytes
+    if ((layout == FP8_TN ? M : K) % 16 != 0 || (layout != FP8_NT ? N : K) % 16 != 0) return FP8_ERR_ALIGNMENT;
+    if (!aligned(a8, 16) || !aligned(b8, 16)) return FP8_ERR_ALIGNMENT;
+    if (stride_a % 16 != 0 || stride_b % 16 != 0) return FP8_ERR_ALIGNMENT;
+    if (!aligned(out, out_align) || !aligned(sa, 4) || !aligned(sb, 4)) return FP8_ERR_ALIGNMENT;
+    if (bias && !bias_scale && !aligned(bias, 2)) return FP8_ERR_ALIGNMENT;
+    return FP8_OK;
 }
 
 }  // namespace

@@ -353,6 +353,68 @@ FP8LITE_API fp8_status fp8_mm_out8(const uint8_t* a8, fp8_fmt fa, const uint8_t*
                   fp8_fmt out_fmt, fp8_ring* out_ring, uint8_t* out8, float* out_amax, float* out_scale,
                   void* stream);
 
+/* Activations of fp8_mm_act, fp8_mm_act_out8, fp8_act_grad and fp8_mm_experts,
+ * computed in fp32:
+ *   RELU       max(z, 0)
+ *   GELU       z Phi(z), Phi the normal distribution function (erf)
+ *   GELU_TANH  z (1 + tanh(sqrt(2/pi) (z + 0.044715 z^3))) / 2
+ *   SILU       z / (1 + exp(-z))
+ * A NaN stays NaN; at -inf and +inf the activations give their limits, 0 and
+ * +inf, and their slopes 0 and 1. */
+typedef enum fp8_act {
+    FP8_ACT_NONE = 0,
+    FP8_ACT_RELU = 1,
+    FP8_ACT_GELU = 2,
+    FP8_ACT_GELU_TANH = 3,
+    FP8_ACT_SILU = 4
+} fp8_act;
+
+/* fp8_mm with an activation and a residual in its epilogue:
+ *
+ *   z[b,i,j]   = (sum_k op(A_b)[i,k] op(B_b)[k,j]) / (sa*sb) + bias_j
+ *   out[b,i,j] = bf16_rne( act(z[b,i,j]) + residual[b,i,j] )
+ *   preact[b,i,j] = bf16_rne( z[b,i,j] )         (what fp8_act_grad reads)
+ *
+ * all in fp32 with the one rounding of each output. The activation sees the
+ * unrounded z. With act NONE it is the product plus the residual: the residual
+ * stream of a block, the sum of two input gradients, a weight gradient added
+ * to the one already there.
+ *
+ * All arguments as fp8_mm, and:
+ * act        fp8_act
+ * residual   NULL, or device bf16[batch*stride_r], row-major [M,N] per batch,
+ *            2-byte aligned. It may be `out` itself with stride_r == stride_c
+ *            (each value is read before it is written); otherwise it must not
+ *            overlap out or preact.
+ * stride_r   elements between consecutive batches of residual: 0 broadcasts
+ *            one matrix to every batch, else >= M*N when batch > 1
+ * preact     NULL, or device bf16[batch*stride_c], laid out as out, 2-byte
+ *            aligned, overlapping no other buffer
+ * Any M and N that fp8_mm takes; with N and the strides multiples of 8 and
+ * out, residual and preact 16-byte aligned the outputs leave as whole tiles
+ * (faster). Never uses a workspace.
+ * Errors: as fp8_mm; FP8_ERR_INVALID_ARG also for a bad act or stride_r. */
+FP8LITE_API fp8_status fp8_mm_act(const uint8_t* a8, fp8_fmt fa, const uint8_t* b8, fp8_fmt fb,
+                  const float* sa, const float* sb, fp8_layout layout,
+                  int64_t M, int64_t N, int64_t K, int64_t batch,
+                  int64_t stride_a, int64_t stride_b, int64_t stride_c,
+                  const void* bias, const float* bias_scale, fp8_fmt bias_fmt,
+                  fp8_act act, const void* residual, int64_t stride_r, void* preact,
+                  void* out, void* stream);
+
+/* fp8_mm_act whose output is the FP8 operand of the next product, as
+ * fp8_mm_out8's: out8[b,i,j] = sat_rne_out_fmt( fp32(act(z[b,i,j]) * s) ) with
+ * s = out_ring->scale as it stood before the call, and the amax of |act(z)|
+ * folded into out_ring. preact as fp8_mm_act; there is no residual.
+ * Errors: as fp8_mm_out8; FP8_ERR_INVALID_ARG also for a bad act. */
+FP8LITE_API fp8_status fp8_mm_act_out8(const uint8_t* a8, fp8_fmt fa, const uint8_t* b8, fp8_fmt fb,
+                  const float* sa, const float* sb, fp8_layout layout,
+                  int64_t M, int64_t N, int64_t K, int64_t batch,
+                  int64_t stride_a, int64_t stride_b, int64_t stride_c,
+                  const void* bias, const float* bias_scale, fp8_fmt bias_fmt,
+                  fp8_act act, void* preact, fp8_fmt out_fmt, fp8_ring* out_ring,
+                  uint8_t* out8, float* out_amax, float* out_scale, void* stream);
+
 /* Workspace bytes fp8_mm_ws needs for this problem and split_k on the
  * current device (split_k 0: for the library's own choice): 0 when that call
  * would not split, or for arguments fp8_mm_ws rejects. */
