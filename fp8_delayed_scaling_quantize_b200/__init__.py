@@ -105,6 +105,7 @@ def _load():
         "fp8_mm_act": (I, [P, I, P, I, P, P, I, I64, I64, I64, I64, I64, I64, I64, P, P, I, I, P, I64, P, P, P]),
         "fp8_mm_act_out8": (I, [P, I, P, I, P, P, I, I64, I64, I64, I64, I64, I64, I64, P, P, I, I, P, I, P, P, P, P,
                                 P]),
+        "fp8_act_grad": (I, [P, P, I64, I64, I, I, P, ctypes.c_uint32, P, P, P, P, P]),
     }
     for name, (res, args) in sig.items():
         try:
@@ -255,6 +256,12 @@ def fp8_mm_act_out8(a8, fa, b8, fb, sa, sb, layout, M, N, K, batch, stride_a, st
                                       _ptr(bias), _ptr(bias_scale), int(bias_fmt), int(act), _ptr(preact),
                                       int(out_fmt), _ptr(out_ring), _ptr(out8), _ptr(out_amax), _ptr(out_scale),
                                       _stream(stream)), "fp8_mm_act_out8")
+
+
+def fp8_act_grad(g, z, rows, cols, act, fmt, ring, flags, out8, amax_out, scale_out, dbias, stream=None):
+    return _check(lib.fp8_act_grad(_ptr(g), _ptr(z), int(rows), int(cols), int(act), int(fmt), _ptr(ring), int(flags),
+                                   _ptr(out8), _ptr(amax_out), _ptr(scale_out), _ptr(dbias), _stream(stream)),
+                  "fp8_act_grad")
 
 
 def fp8_mm_grouped(problems, stream=None):

@@ -79,22 +79,25 @@ __device__ __forceinline__ float act_fwd(float z) {
 template <int ACT>
 __device__ __forceinline__ float act_slope(float z) {
     if (ACT == FP8_ACT_RELU) return z > 0.0f ? 1.0f : 0.0f;
-    z = at_most(at_least(z, -100.0f), 100.0f);
+    // the lower limit keeps 2^x finite below: the slope there is under 2^-100 already
+    z = at_most(at_least(z, ACT == FP8_ACT_GELU_TANH ? -10.0f : ACT == FP8_ACT_SILU ? -87.0f : -100.0f), 100.0f);
     if (ACT == FP8_ACT_GELU) {
         float e;
         const float c = normal_cdf(z, e);
         return fmaf(z, e * 0.3989422804f, c);  // Phi + z phi
     }
+    // y = z s: y' = s + s z (1 - s) w', where s = 1 / (1 + e) and 1 - s = e s (no cancellation)
     if (ACT == FP8_ACT_GELU_TANH) {
-        // y = z s(2u): y' = s + z s (1 - s) 2 u', 2 u' = 2 sqrt(2/pi) (1 + 3 * 0.044715 z^2)
         const float z2 = z * z;
-        const float s = rcp_approx(1.0f + ex2_approx(z * fmaf(z2, kGeluT1, kGeluT0)));
-        const float w = (z * (1.0f - s)) * fmaf(z2, 0.2140644488f, 1.5957691216f);
-        return fmaf(s, w, s);
+        const float e = ex2_approx(z * fmaf(z2, kGeluT1, kGeluT0));
+        const float s = rcp_approx(1.0f + e);
+        // w' = 2 sqrt(2/pi) (1 + 3 * 0.044715 z^2), the derivative of 2u
+        return fmaf(s, (z * (e * s)) * fmaf(z2, 0.2140644488f, 1.5957691216f), s);
     }
     if (ACT == FP8_ACT_SILU) {
-        const float s = rcp_approx(1.0f + ex2_approx(z * -kLog2e));
-        return fmaf(s, z * (1.0f - s), s);
+        const float e = ex2_approx(z * -kLog2e);
+        const float s = rcp_approx(1.0f + e);
+        return fmaf(s, z * (e * s), s);
     }
     return 1.0f;
 }

@@ -1,0 +1,242 @@
+// Gradient through an activation, quantized as it is formed: dz = g act'(z) in
+// fp32, its FP8 codes under a delayed ring, and the bias gradient sum_i dz[i][j].
+//
+// Bound by HBM: 5 bytes an element (g and z in bf16 read, one code written).
+//
+// Split: a cluster of up to 8 CTAs owns a strip of columns, its CTAs taking
+// row blocks in turn, so that a column's sum is finished inside the cluster:
+// each thread adds its rows, the warps meet in shared memory, and rank 0 adds
+// the other CTAs' sums through distributed shared memory. Every sum has one
+// fixed order, in fp32, with no workspace and no atomics; the cluster's amax
+// takes the same way, so the ring sees one atomic per strip. A thread covers
+// 8 columns (16 bytes of g and of z, 8 of codes) of kRows rows at a time.
+
+#include <cuda_runtime.h>
+
+#include "act.cuh"
+#include "common.cuh"
+#include "sm100.cuh"
+
+namespace fp8lite {
+namespace {
+
+using namespace sm100;
+
+constexpr int kThreads = 256;
+constexpr int kWarps = kThreads / 32;
+constexpr int kRows = 4;  // row blocks in flight per thread
+
+struct GradArgs {
+    const uint4* g;
+    const uint4* z;
+    int64_t rows;
+    int64_t pitch;  // 16-byte pieces of a row
+    uint2* out8;
+    fp8_ring* ring;
+    float* amax_out;
+    float* scale_out;
+    uint16_t* dbias;
+    int fmt;
+    int defer;
+    int ranks;  // CTAs of a cluster
+};
+
+__device__ __forceinline__ float lo_f32(uint32_t w) { return __uint_as_float(w << 16); }
+__device__ __forceinline__ float hi_f32(uint32_t w) { return __uint_as_float(w & 0xFFFF0000u); }
+
+__device__ __forceinline__ float ld_cluster_f32(uint32_t addr) {
+    float v;
+    asm volatile("ld.shared::cluster.f32 %0, [%1];" : "=f"(v) : "r"(addr) : "memory");
+    return v;
+}
+
+template <int FMT>
+__device__ __forceinline__ uint32_t cvt2(float lo, float hi) {
+    uint16_t r;
+    if (FMT == FP8_E4M3) asm("cvt.rn.satfinite.e4m3x2.f32 %0, %1, %2;" : "=h"(r) : "f"(hi), "f"(lo));
+    else                 asm("cvt.rn.satfinite.e5m2x2.f32 %0, %1, %2;" : "=h"(r) : "f"(hi), "f"(lo));
+    return r;
+}
+
+template <int FMT>
+__device__ __forceinline__ uint2 codes8(const float (&d)[8], float s) {
+    uint32_t c[4];
+#pragma unroll
+    for (int i = 0; i < 4; ++i) c[i] = cvt2<FMT>(__fmul_rn(d[2 * i], s), __fmul_rn(d[2 * i + 1], s));
+    return make_uint2(c[0] | (c[1] << 16), c[2] | (c[3] << 16));
+}
+
+// W: columns of a strip (64, 32 or 16).
+template <int ACT, int W>
+__global__ void __launch_bounds__(kThreads) act_grad_kernel(const GradArgs a) {
+    constexpr int kTpr = W / 8;                 // threads of a row
+    constexpr int kBlockRows = kThreads / kTpr;  // rows of a block's pass
+    __shared__ float part[kWarps][W];
+    __shared__ float colsum[W];
+    __shared__ uint32_t wmax[kWarps];
+    __shared__ float bmax;
+    __shared__ float s_scale;
+    griddep_wait();
+    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+    const int rank = int(blockIdx.x) % a.ranks;
+    const int64_t strip = int64_t(blockIdx.x) / a.ranks;
+    const int64_t piece = strip * kTpr + threadIdx.x % kTpr;  // this thread's 8 columns
+    const bool in = piece < a.pitch;
+    const int64_t step = int64_t(a.ranks) * kBlockRows;
+    int64_t row = int64_t(rank) * kBlockRows + threadIdx.x / kTpr;
+    uint4 g[kRows], z[kRows];
+    auto load = [&]() {
+#pragma unroll
+        for (int u = 0; u < kRows; ++u) {
+            const int64_t r = row + u * step;
+            if (in && r < a.rows) {
+                g[u] = __ldg(a.g + r * a.pitch + piece);
+                if (ACT != FP8_ACT_NONE) z[u] = __ldg(a.z + r * a.pitch + piece);
+            }
+        }
+    };
+    load();  // before the scale is known: it does not need it
+    if (threadIdx.x == 0) {
+        s_scale = *reinterpret_cast<volatile float*>(&a.ring->scale);
+        if (blockIdx.x == 0) *a.scale_out = s_scale;
+    }
+    __syncthreads();
+    const float s = s_scale;
+    float m = 0.0f, sum[8] = {0.0f, 0.0f, 0.0f, 0.0f, 0.0f, 0.0f, 0.0f, 0.0f};
+    while (row < a.rows) {
+#pragma unroll
+        for (int u = 0; u < kRows; ++u) {
+            const int64_t r = row + u * step;
+            if (in && r < a.rows) {
+                const uint32_t gw[4] = {g[u].x, g[u].y, g[u].z, g[u].w};
+                const uint32_t zw[4] = {z[u].x, z[u].y, z[u].z, z[u].w};
+                float d[8];
+#pragma unroll
+                for (int i = 0; i < 4; ++i) {
+                    d[2 * i] = lo_f32(gw[i]);
+                    d[2 * i + 1] = hi_f32(gw[i]);
+                    if (ACT != FP8_ACT_NONE) {
+                        d[2 * i] *= act_slope<ACT>(lo_f32(zw[i]));
+                        d[2 * i + 1] *= act_slope<ACT>(hi_f32(zw[i]));
+                    }
+                }
+#pragma unroll
+                for (int i = 0; i < 8; ++i) {
+                    m = fmaxf(m, fabsf(d[i]));
+                    sum[i] += d[i];
+                }
+                a.out8[r * a.pitch + piece] = a.fmt == FP8_E4M3 ? codes8<FP8_E4M3>(d, s) : codes8<FP8_E5M2>(d, s);
+            }
+        }
+        row += step * kRows;
+        if (row >= a.rows) break;
+        load();
+    }
+    griddep_launch();
+    // the block's sums and amax
+#pragma unroll
+    for (int i = 0; i < 8; ++i) {
+#pragma unroll
+        for (int o = kTpr; o < 32; o <<= 1) sum[i] += __shfl_xor_sync(0xffffffffu, sum[i], o);
+        if (lane < kTpr) part[warp][lane * 8 + i] = sum[i];
+    }
+    const uint32_t bits = __reduce_max_sync(0xffffffffu, __float_as_uint(m));
+    if (lane == 0) wmax[warp] = bits;
+    __syncthreads();
+    if (threadIdx.x < W) {
+        float v = 0.0f;
+#pragma unroll
+        for (int w = 0; w < kWarps; ++w) v += part[w][threadIdx.x];
+        colsum[threadIdx.x] = v;
+    }
+    if (threadIdx.x == 0) {
+        uint32_t b = wmax[0];
+#pragma unroll
+        for (int w = 1; w < kWarps; ++w) b = max(b, wmax[w]);
+        bmax = __uint_as_float(b);
+    }
+    // the cluster's: rank 0 adds them in rank order
+    cluster_sync();
+    if (rank == 0) {
+        if (threadIdx.x < W && a.dbias) {
+            float v = colsum[threadIdx.x];
+            const uint32_t at = smem_addr(&colsum[threadIdx.x]);
+            for (int r = 1; r < a.ranks; ++r) v += ld_cluster_f32(map_to_rank(at, uint32_t(r)));
+            const int64_t c = strip * W + threadIdx.x;
+            if (c < a.pitch * 8) {
+                uint16_t h;
+                asm("cvt.rn.bf16.f32 %0, %1;" : "=h"(h) : "f"(v));
+                a.dbias[c] = h;
+            }
+        }
+        if (threadIdx.x == 0) {
+            float v = bmax;
+            for (int r = 1; r < a.ranks; ++r) v = fmaxf(v, ld_cluster_f32(map_to_rank(smem_addr(&bmax), uint32_t(r))));
+            fp8_ring* ring = a.ring;
+            if (v != 0.0f) atomicMax(&ring->amax_bits, __float_as_uint(v));
+            const uint32_t ticket = atom_add_acq_rel(&ring->ticket, 1u);
+            if (ticket == gridDim.x / a.ranks - 1) {
+                volatile fp8_ring* rr = ring;
+                if (a.defer) {
+                    if (a.amax_out) *a.amax_out = __uint_as_float(*reinterpret_cast<volatile uint32_t*>(&ring->amax_bits));
+                } else {
+                    float h[FP8_RING_HISTORY];
+                    const uint32_t idx = ring_read(rr, h);
+                    const float top = __uint_as_float(atomicExch(&ring->amax_bits, 0u));
+                    ring_fold(rr, h, idx, top, fmt_max(a.fmt));
+                    if (a.amax_out) *a.amax_out = top;
+                }
+                rr->ticket = 0u;
+            }
+        }
+    }
+    cluster_sync();  // no CTA leaves while rank 0 may still read its shared memory
+}
+
+template <int W>
+fp8_status launch_width(const GradArgs& a, int act, int64_t strips, cudaStream_t st) {
+    const dim3 grid(unsigned(strips * a.ranks));
+    switch (act) {
+        case FP8_ACT_NONE: return launch_pdl(act_grad_kernel<FP8_ACT_NONE, W>, grid, kThreads, 0, st, a.ranks, a);
+        case FP8_ACT_RELU: return launch_pdl(act_grad_kernel<FP8_ACT_RELU, W>, grid, kThreads, 0, st, a.ranks, a);
+        case FP8_ACT_GELU: return launch_pdl(act_grad_kernel<FP8_ACT_GELU, W>, grid, kThreads, 0, st, a.ranks, a);
+        case FP8_ACT_GELU_TANH:
+            return launch_pdl(act_grad_kernel<FP8_ACT_GELU_TANH, W>, grid, kThreads, 0, st, a.ranks, a);
+        default: return launch_pdl(act_grad_kernel<FP8_ACT_SILU, W>, grid, kThreads, 0, st, a.ranks, a);
+    }
+}
+
+}  // namespace
+}  // namespace fp8lite
+
+using namespace fp8lite;
+
+extern "C" fp8_status fp8_act_grad(const void* g, const void* z, int64_t rows, int64_t cols, fp8_act act, fp8_fmt fmt,
+                                   fp8_ring* ring, uint32_t flags, uint8_t* out8, float* amax_out, float* scale_out,
+                                   void* dbias, void* stream) {
+    if (!valid_act(int(act)) || !valid_fmt(int(fmt))) return FP8_ERR_INVALID_ARG;
+    if (flags != 0 && flags != FP8_QUANTIZE_DEFER_FOLD) return FP8_ERR_INVALID_ARG;
+    if (rows < 0 || cols < 1 || cols >= (int64_t(1) << 31) || rows >= (int64_t(1) << 40) / cols)
+        return FP8_ERR_INVALID_ARG;
+    if (!ring || !scale_out) return FP8_ERR_INVALID_ARG;
+    if (rows > 0 && (!g || !out8 || (act != FP8_ACT_NONE && !z))) return FP8_ERR_INVALID_ARG;
+    if (cols % 8 != 0) return FP8_ERR_ALIGNMENT;
+    if (!aligned(g, 16) || !aligned(z, 16) || !aligned(out8, 16) || !aligned(dbias, 2)) return FP8_ERR_ALIGNMENT;
+    if (!aligned(ring, 4) || !aligned(amax_out, 4) || !aligned(scale_out, 4)) return FP8_ERR_ALIGNMENT;
+    GradArgs a = {};
+    a.g = static_cast<const uint4*>(g);
+    a.z = static_cast<const uint4*>(z);
+    a.rows = rows;
+    a.pitch = cols / 8;
+    a.out8 = reinterpret_cast<uint2*>(out8);
+    a.ring = ring;
+    a.amax_out = amax_out;
+    a.scale_out = scale_out;
+    a.dbias = static_cast<uint16_t*>(dbias);
+    a.fmt = int(fmt);
+    a.defer = flags == FP8_QUANTIZE_DEFER_FOLD;
+    const int64_t strips64 = (cols + 63) / 64;
+    // CTAs of a cluster: no more than there are row blocks
+    a.ranks = rows > 128 ? 8 : rows > 64 ? 4 : rows > 32 ? 2 : 1;
+    return launch_width<64>(a, int(act), strips64, as_stream(stream));
+}

@@ -415,6 +415,34 @@ FP8LITE_API fp8_status fp8_mm_act_out8(const uint8_t* a8, fp8_fmt fa, const uint
                   fp8_act act, void* preact, fp8_fmt out_fmt, fp8_ring* out_ring,
                   uint8_t* out8, float* out_amax, float* out_scale, void* stream);
 
+/* Gradient through an activation, quantized in the same pass: the backward
+ * side of fp8_mm_act's activation, in front of the dX and dW products.
+ *
+ *   dz[i,j]   = g[i,j] act'(z[i,j])                        (fp32)
+ *   out8[i,j] = sat_rne_fmt( fp32(dz[i,j] * s) ),  s = ring->scale as it stood
+ *               before the call (reported in *scale_out)
+ *   dbias[j]  = bf16_rne( sum_i dz[i,j] )      (fp32 sums in a fixed order)
+ *
+ * and the amax of the unquantized |dz| (NaN ignored) is folded into the ring as
+ * a delayed fp8_quantize call folds its input's. ReLU's slope at 0 is 0. With
+ * act NONE dz is g: fp8_quantize and fp8_bias_grad in one pass.
+ *
+ * g, z       device bf16[rows, cols], row-major, 16-byte aligned. z is the
+ *            activation's input (fp8_mm_act's preact); unused with act NONE
+ * rows, cols rows >= 0 (0 folds amax 0 and gives dbias 0), cols >= 1 and a
+ *            multiple of 8, rows * cols < 2^40
+ * ring       required; one call at a time may use it
+ * flags      0 or FP8_QUANTIZE_DEFER_FOLD (the amax stays in the ring's
+ *            accumulator for a data-parallel exchange; see fp8_quantize_ex)
+ * out8       device uint8[rows, cols], 16-byte aligned
+ * amax_out   optional; scale_out required
+ * dbias      NULL, or device bf16[cols], 2-byte aligned
+ * Errors: FP8_ERR_INVALID_ARG, FP8_ERR_ALIGNMENT (also for cols not a multiple
+ *         of 8), FP8_ERR_CUDA. */
+FP8LITE_API fp8_status fp8_act_grad(const void* g, const void* z, int64_t rows, int64_t cols, fp8_act act,
+                        fp8_fmt fmt, fp8_ring* ring, uint32_t flags, uint8_t* out8, float* amax_out,
+                        float* scale_out, void* dbias, void* stream);
+
 /* Workspace bytes fp8_mm_ws needs for this problem and split_k on the
  * current device (split_k 0: for the library's own choice): 0 when that call
  * would not split, or for arguments fp8_mm_ws rejects. */
