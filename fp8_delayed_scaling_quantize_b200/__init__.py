@@ -60,6 +60,7 @@ class fp8_quantize_job(ctypes.Structure):
 assert ctypes.sizeof(fp8_quantize_job) == 56
 
 FP8_MM_MAX_GROUP = 4
+FP8_MM_MAX_EXPERTS = 512
 
 
 class fp8_mm_problem(ctypes.Structure):
@@ -105,6 +106,7 @@ def _load():
         "fp8_mm_act": (I, [P, I, P, I, P, P, I, I64, I64, I64, I64, I64, I64, I64, P, P, I, I, P, I64, P, P, P]),
         "fp8_mm_act_out8": (I, [P, I, P, I, P, P, I, I64, I64, I64, I64, I64, I64, I64, P, P, I, I, P, I, P, P, P, P,
                                 P]),
+        "fp8_mm_experts": (I, [P, I, P, I, P, P, ctypes.c_int32, I, I64, I64, I64, ctypes.c_int32, P, P, I, P, P, P]),
         "fp8_act_grad": (I, [P, P, I64, I64, I, I, P, ctypes.c_uint32, P, P, P, P, P]),
     }
     for name, (res, args) in sig.items():
@@ -256,6 +258,13 @@ def fp8_mm_act_out8(a8, fa, b8, fb, sa, sb, layout, M, N, K, batch, stride_a, st
                                       _ptr(bias), _ptr(bias_scale), int(bias_fmt), int(act), _ptr(preact),
                                       int(out_fmt), _ptr(out_ring), _ptr(out8), _ptr(out_amax), _ptr(out_scale),
                                       _stream(stream)), "fp8_mm_act_out8")
+
+
+def fp8_mm_experts(a8, fa, b8, fb, sa, sb, sb_stride, layout, M, N, K, experts, offsets, bias, act, preact, out,
+                   stream=None):
+    return _check(lib.fp8_mm_experts(_ptr(a8), int(fa), _ptr(b8), int(fb), _ptr(sa), _ptr(sb), int(sb_stride),
+                                     int(layout), int(M), int(N), int(K), int(experts), _ptr(offsets), _ptr(bias),
+                                     int(act), _ptr(preact), _ptr(out), _stream(stream)), "fp8_mm_experts")
 
 
 def fp8_act_grad(g, z, rows, cols, act, fmt, ring, flags, out8, amax_out, scale_out, dbias, stream=None):

@@ -7,5 +7,6 @@
 namespace fp8lite {
 
 bool gemm_act_error(uint32_t* v);
+bool experts_error(uint32_t* v);
 
 }  // namespace fp8lite

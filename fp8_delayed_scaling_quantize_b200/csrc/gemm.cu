@@ -425,9 +425,9 @@ extern "C" fp8_status fp8_mm_splitk_static(const uint8_t* a8, fp8_fmt fa, const 
 
 extern "C" fp8_status fp8_last_device_error(void) {
     if (cudaDeviceSynchronize() != cudaSuccess) return FP8_ERR_CUDA;
-    uint32_t v = 0, w = 0;
-    if (!take_error_word(&v) || !gemm_act_error(&w)) return FP8_ERR_CUDA;
-    return (v | w) ? FP8_ERR_DEVICE_TIMEOUT : FP8_OK;
+    uint32_t v[3] = {0, 0, 0};
+    if (!take_error_word(&v[0]) || !gemm_act_error(&v[1]) || !experts_error(&v[2])) return FP8_ERR_CUDA;
+    return (v[0] | v[1] | v[2]) ? FP8_ERR_DEVICE_TIMEOUT : FP8_OK;
 }
 
 extern "C" fp8_status fp8_selftest_wait_timeout(uint32_t limit_us, void* stream) {

@@ -443,6 +443,53 @@ FP8LITE_API fp8_status fp8_act_grad(const void* g, const void* z, int64_t rows, 
                         fp8_fmt fmt, fp8_ring* ring, uint32_t flags, uint8_t* out8, float* amax_out,
                         float* scale_out, void* dbias, void* stream);
 
+/* FP8 products grouped by expert, in ONE launch: the rows of a token-sorted
+ * matrix belong to `experts` experts in turn, rows [offsets[e], offsets[e+1])
+ * to expert e, and every expert multiplies them with its own weight. The
+ * offsets are read on the device: nothing is synchronised, and a captured call
+ * follows the offsets of each replay. `layout` names the product of a linear
+ * layer, and one of M, N, K is the number of token rows of ALL experts:
+ *
+ *   FP8_NT  M rows: A [M,K], B [experts][N,K]   (forward)
+ *           out[r] = bf16_rne( act(z[r]) ), preact[r] = bf16_rne( z[r] ),
+ *           z[r] = (A[r] B[e]^T) / (sa*sb_e) + bias[e]     for r in e's rows
+ *   FP8_NN  M rows: A [M,K], B [experts][K,N]   (input gradient; the same with
+ *           z[r] = (A[r] B[e]) / (sa*sb_e) + bias[e])
+ *   FP8_TN  K rows: A [K,M], B [K,N], out [experts][M,N]   (weight gradient)
+ *           out[e] = bf16_rne( (A[e's rows]^T B[e's rows]) / (sa*sb) )
+ *           an expert without rows gets zeros
+ *
+ * in fp32 with the one rounding of each output, as fp8_mm. Rows before
+ * offsets[0] and from offsets[experts] on belong to no expert: NT and NN leave
+ * them in out and preact as they are, TN does not read them.
+ *
+ * a8, b8     FP8 codes of formats fa, fb, 16-byte aligned
+ * sa         device float: A's scale
+ * sb         device float (sb_stride 0: one scale for all of B) or float[experts]
+ *            (sb_stride 1: one for each expert's weight; NT and NN)
+ * M, N, K    >= 1, the token rows >= 0, each < 2^31. Multiples of 16: K in NT,
+ *            K and N in NN, M and N in TN; the token rows and N in NT are free.
+ * experts    1 .. FP8_MM_MAX_EXPERTS
+ * offsets    device int32[experts + 1], 4-byte aligned, not decreasing, within
+ *            [0, token rows]. Others cannot be refused (they are on the
+ *            device): each is limited to that range and to no less than the
+ *            one before it, so that nothing outside the buffers is touched.
+ * bias       NULL, or device bf16[experts][N] (NT, NN)
+ * act        fp8_act (NT, NN; NONE in TN)
+ * preact     NULL, or device bf16[M,N] (NT, NN)
+ * out        device bf16; as preact 2-byte aligned, overlapping no other
+ *            buffer. With N a multiple of 8 and out and preact 16-byte
+ *            aligned the outputs leave as whole tiles (faster).
+ * No workspace. Errors: FP8_ERR_INVALID_ARG (also bias, preact, an activation
+ * or sb_stride 1 in TN), FP8_ERR_ALIGNMENT, FP8_ERR_UNSUPPORTED (a size >= 2^31
+ * or more experts), FP8_ERR_CUDA. A bounded device wait that gives up is
+ * reported by fp8_last_device_error. */
+#define FP8_MM_MAX_EXPERTS 512
+FP8LITE_API fp8_status fp8_mm_experts(const uint8_t* a8, fp8_fmt fa, const uint8_t* b8, fp8_fmt fb,
+                  const float* sa, const float* sb, int32_t sb_stride, fp8_layout layout,
+                  int64_t M, int64_t N, int64_t K, int32_t experts, const int32_t* offsets,
+                  const void* bias, fp8_act act, void* preact, void* out, void* stream);
+
 /* Workspace bytes fp8_mm_ws needs for this problem and split_k on the
  * current device (split_k 0: for the library's own choice): 0 when that call
  * would not split, or for arguments fp8_mm_ws rejects. */
