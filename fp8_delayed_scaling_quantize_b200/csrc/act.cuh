@@ -2,7 +2,12 @@
 // fp32. sigmoid(x) = 1 / (1 + 2^(-x log2 e)) takes the two MUFU instructions
 // ex2.approx and rcp.approx, whose documented errors are 2 ulp and 1 ulp: the
 // results are within a few 2^-23 of the formula (relative to z), far below
-// the bf16 or FP8 rounding that follows.
+// the bf16 or FP8 rounding that follows. Their .ftz forms are one instruction
+// each, where the others scale subnormals around it; only results below
+// 2^-126 are flushed. Everything else runs on pairs (fma.rn.f32x2 and its
+// like), which rounds each half as the scalar instruction would at half the
+// instructions: the epilogues and the gradient are bound by issue before they
+// are by MUFU.
 //   ReLU       z < 0 ? 0 : z                       (NaN stays NaN)
 //   GELU       z Phi(z), Phi(z) = (1 + erf(z / sqrt 2)) / 2, erf by the
 //              rational form 7.1.26 of Abramowitz and Stegun's handbook
@@ -18,30 +23,52 @@ namespace fp8lite {
 
 inline bool valid_act(int a) { return a >= FP8_ACT_NONE && a <= FP8_ACT_SILU; }
 
-__device__ __forceinline__ float ex2_approx(float x) {
-    float y;
-    asm("ex2.approx.f32 %0, %1;" : "=f"(y) : "f"(x));
-    return y;
+// Two fp32 values in one 64-bit register pair.
+using F2 = unsigned long long;
+
+__device__ __forceinline__ F2 f2(float lo, float hi) {
+    F2 r;
+    asm("mov.b64 %0, {%1, %2};" : "=l"(r) : "f"(lo), "f"(hi));
+    return r;
+}
+__device__ __forceinline__ F2 f2(float v) { return f2(v, v); }
+__device__ __forceinline__ void split(F2 v, float& lo, float& hi) {
+    asm("mov.b64 {%0, %1}, %2;" : "=f"(lo), "=f"(hi) : "l"(v));
+}
+__device__ __forceinline__ F2 mul2(F2 a, F2 b) {
+    F2 r;
+    asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
+    return r;
+}
+__device__ __forceinline__ F2 add2(F2 a, F2 b) {
+    F2 r;
+    asm("add.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
+    return r;
+}
+__device__ __forceinline__ F2 fma2(F2 a, F2 b, F2 c) {
+    F2 r;
+    asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(r) : "l"(a), "l"(b), "l"(c));
+    return r;
+}
+__device__ __forceinline__ F2 ex2_2(F2 x) {
+    float a, b;
+    split(x, a, b);
+    asm("ex2.approx.ftz.f32 %0, %0;" : "+f"(a));
+    asm("ex2.approx.ftz.f32 %0, %0;" : "+f"(b));
+    return f2(a, b);
+}
+__device__ __forceinline__ F2 rcp2(F2 x) {
+    float a, b;
+    split(x, a, b);
+    asm("rcp.approx.ftz.f32 %0, %0;" : "+f"(a));
+    asm("rcp.approx.ftz.f32 %0, %0;" : "+f"(b));
+    return f2(a, b);
 }
 
-__device__ __forceinline__ float rcp_approx(float x) {
-    float y;
-    asm("rcp.approx.f32 %0, %1;" : "=f"(y) : "f"(x));
-    return y;
-}
-
-// max / min that keep a NaN. Below -100 (and above 100) every activation here
-// is 0 (z) and every slope 0 (1) in fp32: limiting z to that range first gives
-// the limits also at infinities, where the formulas would multiply 0 by inf.
+// max that keeps a NaN.
 __device__ __forceinline__ float at_least(float x, float lo) {
     float y;
     asm("max.NaN.f32 %0, %1, %2;" : "=f"(y) : "f"(x), "f"(lo));
-    return y;
-}
-
-__device__ __forceinline__ float at_most(float x, float hi) {
-    float y;
-    asm("min.NaN.f32 %0, %1, %2;" : "=f"(y) : "f"(x), "f"(hi));
     return y;
 }
 
@@ -51,74 +78,84 @@ constexpr float kGeluT0 = -2.3022081985f;
 constexpr float kGeluT1 = -0.1029432396f;
 
 // Phi(z), the standard normal distribution function; e is exp(-z^2 / 2).
-__device__ __forceinline__ float normal_cdf(float z, float& e) {
-    const float a = fabsf(z);
-    const float t = rcp_approx(fmaf(a, 0.23164189f, 1.0f));  // 0.3275911 / sqrt 2
-    e = ex2_approx(z * z * (-0.5f * kLog2e));
+__device__ __forceinline__ F2 normal_cdf(F2 z, F2& e) {
+    const F2 t = rcp2(fma2(z & 0x7FFFFFFF7FFFFFFFull, f2(0.23164189f), f2(1.0f)));  // 0.3275911 / sqrt 2
+    e = ex2_2(mul2(mul2(z, z), f2(-0.5f * kLog2e)));
     // half of (a1 t + a2 t^2 + a3 t^3 + a4 t^4 + a5 t^5)
-    const float p = t * fmaf(t, fmaf(t, fmaf(t, fmaf(t, 0.5307027145f, -0.7265760135f), 0.7107068705f), -0.142248368f),
-                             0.127414796f);
-    const float q = p * e;
-    return z < 0.0f ? q : 1.0f - q;
+    F2 p = fma2(t, f2(0.5307027145f), f2(-0.7265760135f));
+    p = fma2(t, p, f2(0.7107068705f));
+    p = fma2(t, p, f2(-0.142248368f));
+    p = fma2(t, p, f2(0.127414796f));
+    const F2 q = mul2(mul2(t, p), e);
+    float z0, z1, q0, q1, r0, r1;
+    split(z, z0, z1);
+    split(q, q0, q1);
+    split(fma2(q, f2(-1.0f), f2(1.0f)), r0, r1);
+    return f2(z0 < 0.0f ? q0 : r0, z1 < 0.0f ? q1 : r1);
 }
 
+// act(z). Below -100 every activation but ReLU is 0 in fp32: limiting z first
+// gives that also at -inf, where the formula would multiply it by 0.
 template <int ACT>
-__device__ __forceinline__ float act_fwd(float z) {
-    if (ACT == FP8_ACT_RELU) return z < 0.0f ? 0.0f : z;
-    if (ACT != FP8_ACT_NONE) z = at_least(z, -100.0f);
+__device__ __forceinline__ F2 act_fwd(F2 z) {
+    if (ACT == FP8_ACT_NONE) return z;
+    float a, b;
+    split(z, a, b);
+    if (ACT == FP8_ACT_RELU) return f2(a < 0.0f ? 0.0f : a, b < 0.0f ? 0.0f : b);
+    z = f2(at_least(a, -100.0f), at_least(b, -100.0f));
     if (ACT == FP8_ACT_GELU) {
-        float e;
-        return z * normal_cdf(z, e);
+        F2 e;
+        return mul2(z, normal_cdf(z, e));
     }
-    if (ACT == FP8_ACT_GELU_TANH) return z * rcp_approx(1.0f + ex2_approx(z * fmaf(z * z, kGeluT1, kGeluT0)));
-    if (ACT == FP8_ACT_SILU) return z * rcp_approx(1.0f + ex2_approx(z * -kLog2e));
-    return z;
+    const F2 x = ACT == FP8_ACT_GELU_TANH ? mul2(z, fma2(mul2(z, z), f2(kGeluT1), f2(kGeluT0))) : mul2(z, f2(-kLog2e));
+    return mul2(z, rcp2(add2(ex2_2(x), f2(1.0f))));
 }
 
-// act'(z).
+// act'(z) of a pair of bf16 values, the first in the low half. z is limited
+// to a range outside which the slope is 0 or 1 in fp32 (under 2^-100 off),
+// so that 2^x below stays finite and infinities give the limits.
 template <int ACT>
-__device__ __forceinline__ float act_slope(float z) {
-    if (ACT == FP8_ACT_RELU) return z > 0.0f ? 1.0f : 0.0f;
-    // the lower limit keeps 2^x finite below: the slope there is under 2^-100 already
-    z = at_most(at_least(z, ACT == FP8_ACT_GELU_TANH ? -10.0f : ACT == FP8_ACT_SILU ? -87.0f : -100.0f), 100.0f);
+__device__ __forceinline__ F2 act_slope(uint32_t zz) {
+    if (ACT == FP8_ACT_NONE) return f2(1.0f);
+    // bf16 pairs: 100; -10 (GELU tanh), -87 (SiLU), -100 (GELU)
+    constexpr uint32_t kLo = ACT == FP8_ACT_GELU_TANH ? 0xC120C120u : ACT == FP8_ACT_SILU ? 0xC2AEC2AEu : 0xC2C8C2C8u;
+    if (ACT != FP8_ACT_RELU)
+        asm("max.NaN.bf16x2 %0, %0, %1;\n\tmin.NaN.bf16x2 %0, %0, %2;" : "+r"(zz) : "r"(kLo), "r"(0x42C842C8u));
+    const float z0 = __uint_as_float(zz << 16), z1 = __uint_as_float(zz & 0xFFFF0000u);
+    if (ACT == FP8_ACT_RELU) return f2(z0 > 0.0f ? 1.0f : 0.0f, z1 > 0.0f ? 1.0f : 0.0f);
+    const F2 z = f2(z0, z1);
     if (ACT == FP8_ACT_GELU) {
-        float e;
-        const float c = normal_cdf(z, e);
-        return fmaf(z, e * 0.3989422804f, c);  // Phi + z phi
+        F2 e;
+        const F2 c = normal_cdf(z, e);
+        return fma2(z, mul2(e, f2(0.3989422804f)), c);  // Phi + z phi
     }
     // y = z s: y' = s + s z (1 - s) w', where s = 1 / (1 + e) and 1 - s = e s (no cancellation)
     if (ACT == FP8_ACT_GELU_TANH) {
-        const float z2 = z * z;
-        const float e = ex2_approx(z * fmaf(z2, kGeluT1, kGeluT0));
-        const float s = rcp_approx(1.0f + e);
+        const F2 zsq = mul2(z, z);
+        const F2 e = ex2_2(mul2(z, fma2(zsq, f2(kGeluT1), f2(kGeluT0))));
+        const F2 s = rcp2(add2(e, f2(1.0f)));
         // w' = 2 sqrt(2/pi) (1 + 3 * 0.044715 z^2), the derivative of 2u
-        return fmaf(s, (z * (e * s)) * fmaf(z2, 0.2140644488f, 1.5957691216f), s);
+        return fma2(s, mul2(mul2(z, mul2(e, s)), fma2(zsq, f2(0.2140644488f), f2(1.5957691216f))), s);
     }
-    if (ACT == FP8_ACT_SILU) {
-        const float e = ex2_approx(z * -kLog2e);
-        const float s = rcp_approx(1.0f + e);
-        return fmaf(s, z * (e * s), s);
-    }
-    return 1.0f;
+    const F2 e = ex2_2(mul2(z, f2(-kLog2e)));
+    const F2 s = rcp2(add2(e, f2(1.0f)));
+    return fma2(s, mul2(z, mul2(e, s)), s);
+}
+
+template <int ACT, int N>
+__device__ __forceinline__ void act_each(float (&y)[N]) {
+#pragma unroll
+    for (int i = 0; i < N; i += 2) split(act_fwd<ACT>(f2(y[i], y[i + 1])), y[i], y[i + 1]);
 }
 
 // One activation over the values of a register array; the choice is uniform
 // over the launch, so it costs one branch per call.
 template <int N>
 __device__ __forceinline__ void act_apply(int act, float (&y)[N]) {
-    if (act == FP8_ACT_RELU) {
-#pragma unroll
-        for (int i = 0; i < N; ++i) y[i] = act_fwd<FP8_ACT_RELU>(y[i]);
-    } else if (act == FP8_ACT_GELU) {
-#pragma unroll
-        for (int i = 0; i < N; ++i) y[i] = act_fwd<FP8_ACT_GELU>(y[i]);
-    } else if (act == FP8_ACT_GELU_TANH) {
-#pragma unroll
-        for (int i = 0; i < N; ++i) y[i] = act_fwd<FP8_ACT_GELU_TANH>(y[i]);
-    } else if (act == FP8_ACT_SILU) {
-#pragma unroll
-        for (int i = 0; i < N; ++i) y[i] = act_fwd<FP8_ACT_SILU>(y[i]);
-    }
+    if (act == FP8_ACT_RELU) act_each<FP8_ACT_RELU>(y);
+    else if (act == FP8_ACT_GELU) act_each<FP8_ACT_GELU>(y);
+    else if (act == FP8_ACT_GELU_TANH) act_each<FP8_ACT_GELU_TANH>(y);
+    else if (act == FP8_ACT_SILU) act_each<FP8_ACT_SILU>(y);
 }
 
 }  // namespace fp8lite

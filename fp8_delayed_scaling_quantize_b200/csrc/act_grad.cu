@@ -24,7 +24,9 @@ using namespace sm100;
 
 constexpr int kThreads = 256;
 constexpr int kWarps = kThreads / 32;
-constexpr int kRows = 4;  // row blocks in flight per thread
+constexpr int kRows = 2;   // rows in flight per thread
+constexpr int kPerSm = 4;  // CTAs of an SM
+constexpr int kMaxRanks = 8;  // CTAs of a cluster
 
 struct GradArgs {
     const uint4* g;
@@ -59,16 +61,28 @@ __device__ __forceinline__ uint32_t cvt2(float lo, float hi) {
 }
 
 template <int FMT>
-__device__ __forceinline__ uint2 codes8(const float (&d)[8], float s) {
+__device__ __forceinline__ uint2 codes8(const F2 (&d)[4], float s) {
     uint32_t c[4];
 #pragma unroll
-    for (int i = 0; i < 4; ++i) c[i] = cvt2<FMT>(__fmul_rn(d[2 * i], s), __fmul_rn(d[2 * i + 1], s));
+    for (int i = 0; i < 4; ++i) {
+        float lo, hi;
+        split(mul2(d[i], f2(s)), lo, hi);
+        c[i] = cvt2<FMT>(lo, hi);
+    }
     return make_uint2(c[0] | (c[1] << 16), c[2] | (c[3] << 16));
+}
+
+// max(m, |lo|, |hi|); NaN is ignored.
+__device__ __forceinline__ float max_abs(float m, F2 v) {
+    float lo, hi;
+    split(v, lo, hi);
+    asm("max.abs.f32 %0, %0, %1, %2;" : "+f"(m) : "f"(lo), "f"(hi));
+    return m;
 }
 
 // W: columns of a strip (64, 32 or 16).
 template <int ACT, int W>
-__global__ void __launch_bounds__(kThreads) act_grad_kernel(const GradArgs a) {
+__global__ void __launch_bounds__(kThreads, kPerSm) act_grad_kernel(const GradArgs a) {
     constexpr int kTpr = W / 8;                 // threads of a row
     constexpr int kBlockRows = kThreads / kTpr;  // rows of a block's pass
     __shared__ float part[kWarps][W];
@@ -82,63 +96,73 @@ __global__ void __launch_bounds__(kThreads) act_grad_kernel(const GradArgs a) {
     const int64_t strip = int64_t(blockIdx.x) / a.ranks;
     const int64_t piece = strip * kTpr + threadIdx.x % kTpr;  // this thread's 8 columns
     const bool in = piece < a.pitch;
-    const int64_t step = int64_t(a.ranks) * kBlockRows;
-    int64_t row = int64_t(rank) * kBlockRows + threadIdx.x / kTpr;
+    const int64_t step = int64_t(a.ranks) * kBlockRows;  // rows between two of this thread
+    const int64_t row = int64_t(rank) * kBlockRows + threadIdx.x / kTpr;
+    int n = in && row < a.rows ? int((a.rows - row + step - 1) / step) : 0;  // rows left
+    int64_t at = row * a.pitch + piece;
+    const int64_t stride = step * a.pitch;
+    const uint4* pg = a.g + at;  // the row to load next
+    const uint4* pz = a.z + at;
     uint4 g[kRows], z[kRows];
-    auto load = [&]() {
-#pragma unroll
-        for (int u = 0; u < kRows; ++u) {
-            const int64_t r = row + u * step;
-            if (in && r < a.rows) {
-                g[u] = __ldg(a.g + r * a.pitch + piece);
-                if (ACT != FP8_ACT_NONE) z[u] = __ldg(a.z + r * a.pitch + piece);
-            }
+    auto load = [&](int u) {
+        g[u] = __ldg(pg);
+        pg += stride;
+        if (ACT != FP8_ACT_NONE) {
+            z[u] = __ldg(pz);
+            pz += stride;
         }
     };
-    load();  // before the scale is known: it does not need it
+#pragma unroll
+    for (int u = 0; u < kRows; ++u)
+        if (u < n) load(u);  // before the scale is known: the loads do not need it
     if (threadIdx.x == 0) {
         s_scale = *reinterpret_cast<volatile float*>(&a.ring->scale);
         if (blockIdx.x == 0) *a.scale_out = s_scale;
     }
     __syncthreads();
     const float s = s_scale;
-    float m = 0.0f, sum[8] = {0.0f, 0.0f, 0.0f, 0.0f, 0.0f, 0.0f, 0.0f, 0.0f};
-    while (row < a.rows) {
+    float m = 0.0f;
+    F2 sum[4] = {0, 0, 0, 0};
+    uint2* out = a.out8 + at;
+    while (n > 0) {
 #pragma unroll
         for (int u = 0; u < kRows; ++u) {
-            const int64_t r = row + u * step;
-            if (in && r < a.rows) {
+            if (u < n) {
                 const uint32_t gw[4] = {g[u].x, g[u].y, g[u].z, g[u].w};
                 const uint32_t zw[4] = {z[u].x, z[u].y, z[u].z, z[u].w};
-                float d[8];
+                F2 d[4];
 #pragma unroll
                 for (int i = 0; i < 4; ++i) {
-                    d[2 * i] = lo_f32(gw[i]);
-                    d[2 * i + 1] = hi_f32(gw[i]);
-                    if (ACT != FP8_ACT_NONE) {
-                        d[2 * i] *= act_slope<ACT>(lo_f32(zw[i]));
-                        d[2 * i + 1] *= act_slope<ACT>(hi_f32(zw[i]));
-                    }
+                    d[i] = f2(lo_f32(gw[i]), hi_f32(gw[i]));
+                    if (ACT != FP8_ACT_NONE) d[i] = mul2(d[i], act_slope<ACT>(zw[i]));
                 }
+                if (u + kRows < n) load(u);  // the registers are free: the row kRows further on
 #pragma unroll
-                for (int i = 0; i < 8; ++i) {
-                    m = fmaxf(m, fabsf(d[i]));
-                    sum[i] += d[i];
+                for (int i = 0; i < 4; ++i) {
+                    m = max_abs(m, d[i]);
+                    sum[i] = add2(sum[i], d[i]);
                 }
-                a.out8[r * a.pitch + piece] = a.fmt == FP8_E4M3 ? codes8<FP8_E4M3>(d, s) : codes8<FP8_E5M2>(d, s);
+                *out = a.fmt == FP8_E4M3 ? codes8<FP8_E4M3>(d, s) : codes8<FP8_E5M2>(d, s);
+                out += stride;
             }
         }
-        row += step * kRows;
-        if (row >= a.rows) break;
-        load();
+        n -= kRows;
     }
     griddep_launch();
     // the block's sums and amax
 #pragma unroll
-    for (int i = 0; i < 8; ++i) {
+    for (int i = 0; i < 4; ++i) {
+        float v0, v1;
+        split(sum[i], v0, v1);
 #pragma unroll
-        for (int o = kTpr; o < 32; o <<= 1) sum[i] += __shfl_xor_sync(0xffffffffu, sum[i], o);
-        if (lane < kTpr) part[warp][lane * 8 + i] = sum[i];
+        for (int o = kTpr; o < 32; o <<= 1) {
+            v0 += __shfl_xor_sync(0xffffffffu, v0, o);
+            v1 += __shfl_xor_sync(0xffffffffu, v1, o);
+        }
+        if (lane < kTpr) {
+            part[warp][lane * 8 + 2 * i] = v0;
+            part[warp][lane * 8 + 2 * i + 1] = v1;
+        }
     }
     const uint32_t bits = __reduce_max_sync(0xffffffffu, __float_as_uint(m));
     if (lane == 0) wmax[warp] = bits;
@@ -216,7 +240,8 @@ extern "C" fp8_status fp8_act_grad(const void* g, const void* z, int64_t rows, i
                                    void* dbias, void* stream) {
     if (!valid_act(int(act)) || !valid_fmt(int(fmt))) return FP8_ERR_INVALID_ARG;
     if (flags != 0 && flags != FP8_QUANTIZE_DEFER_FOLD) return FP8_ERR_INVALID_ARG;
-    if (rows < 0 || cols < 1 || cols >= (int64_t(1) << 31) || rows >= (int64_t(1) << 40) / cols)
+    if (rows < 0 || cols < 1 || cols >= (int64_t(1) << 31) || rows >= (int64_t(1) << 31) ||
+        rows >= (int64_t(1) << 40) / cols)
         return FP8_ERR_INVALID_ARG;
     if (!ring || !scale_out) return FP8_ERR_INVALID_ARG;
     if (rows > 0 && (!g || !out8 || (act != FP8_ACT_NONE && !z))) return FP8_ERR_INVALID_ARG;
@@ -235,8 +260,16 @@ extern "C" fp8_status fp8_act_grad(const void* g, const void* z, int64_t rows, i
     a.dbias = static_cast<uint16_t*>(dbias);
     a.fmt = int(fmt);
     a.defer = flags == FP8_QUANTIZE_DEFER_FOLD;
-    const int64_t strips64 = (cols + 63) / 64;
-    // CTAs of a cluster: no more than there are row blocks
-    a.ranks = rows > 128 ? 8 : rows > 64 ? 4 : rows > 32 ? 2 : 1;
-    return launch_width<64>(a, int(act), strips64, as_stream(stream));
+    // Strips of 64 columns (a row piece is one 128-byte line) unless they are
+    // too few to give every SM two CTAs; as many CTAs to a strip as stay
+    // resident together and have rows.
+    const auto strips = [&](int w) { return (cols + w - 1) / w; };
+    const int w = strips(64) * kMaxRanks >= 2 * 148 ? 64 : strips(32) * kMaxRanks >= 2 * 148 ? 32 : 16;
+    const int64_t blocks = (rows + kThreads / (w / 8) - 1) / (kThreads / (w / 8));
+    a.ranks = 1;
+    while (a.ranks < kMaxRanks && a.ranks < blocks && strips(w) * a.ranks * 2 <= kPerSm * 148) a.ranks *= 2;
+    cudaStream_t st = as_stream(stream);
+    if (w == 64) return launch_width<64>(a, int(act), strips(64), st);
+    if (w == 32) return launch_width<32>(a, int(act), strips(32), st);
+    return launch_width<16>(a, int(act), strips(16), st);
 }

@@ -430,7 +430,7 @@ FP8LITE_API fp8_status fp8_mm_act_out8(const uint8_t* a8, fp8_fmt fa, const uint
  * g, z       device bf16[rows, cols], row-major, 16-byte aligned. z is the
  *            activation's input (fp8_mm_act's preact); unused with act NONE
  * rows, cols rows >= 0 (0 folds amax 0 and gives dbias 0), cols >= 1 and a
- *            multiple of 8, rows * cols < 2^40
+ *            multiple of 8, each < 2^31, rows * cols < 2^40
  * ring       required; one call at a time may use it
  * flags      0 or FP8_QUANTIZE_DEFER_FOLD (the amax stays in the ring's
  *            accumulator for a data-parallel exchange; see fp8_quantize_ex)
