@@ -6,9 +6,8 @@
 //   NT, NN   out[r] = act(A[r] op(B[e]) / (sa sb_e) + bias_e),  r in e's rows
 //   TN       out[e] = A[rows of e]^T B[rows of e] / (sa sb)
 //
-// One persistent launch. Each CTA turns the offsets into a table of tiles per
-// expert in shared memory (clamped to the matrix and made monotone first, so
-// that no offsets can lead an access out of it) and walks its share of the
+// One persistent launch. Each warp of a CTA works out from the offsets which
+// expert a unit belongs to (struct Experts) and walks the CTA's share of the
 // units; the roles, pipeline and epilogue are those of gemm_kernel.cuh.
 //
 //  * A tile that reaches past its expert's last row loads the next expert's
@@ -65,100 +64,151 @@ struct Item {
     int k_row, k_end;  // SUM: the expert's rows
 };
 
-// The tile table of a CTA.
-struct Table {
-    int off[kMaxExperts + 1];
-    int tiles[kMaxExperts + 1];  // tiles (ROWS) before each expert
-};
+// Where the experts' rows begin and end, looked up by a whole warp (every lane
+// calls every function, with the same arguments). A lane stands for `per`
+// consecutive experts and knows the tiles before them, so that a lookup is a
+// ballot over the lanes and one over the experts of the lane found, whose
+// offsets come from L1 then: no table in shared memory, and no block barrier
+// before the first load. Offsets are limited to [0, rows] and to no less than
+// the one before (a running maximum), so that no offsets lead an access out
+// of the matrices.
+template <int TILE>  // rows of a tile
+struct Experts {
+    const int32_t* offsets;
+    int experts, rows, per, lane;
+    int before;  // maximum of the offsets before this lane's
+    int tiles;   // tiles up to and with this lane's experts
+    int mine;    // this lane's
+    // the expert found last: its tiles [t0, t1) and rows [lo, hi)
+    int e, t0, t1, lo, hi;
 
-// Fills the table (every thread of the block calls it). TILE: rows of a tile.
-template <int TILE>
-__device__ __forceinline__ void build_table(Table& tab, const ExpertParams& p) {
-    const int n = p.experts + 1;
-    for (int i = threadIdx.x; i < n; i += blockDim.x) tab.off[i] = min(max(__ldg(p.offsets + i), 0), p.rows);
-    __syncthreads();
-    if (threadIdx.x < 32) {
-        const int lane = threadIdx.x, per = (n + 31) / 32;
-        const int lo = min(lane * per, n), hi = min(lo + per, n);
-        // running maximum: expert e ends where the next begins, never before it
+    __device__ __forceinline__ int at(int i) const { return min(max(__ldg(offsets + min(i, experts)), 0), rows); }
+    __device__ __forceinline__ static int count(int lo, int hi) { return (hi - lo + TILE - 1) / TILE; }
+
+    __device__ __forceinline__ void init(const ExpertParams& p) {
+        offsets = p.offsets;
+        experts = p.experts;
+        rows = p.rows;
+        per = (experts + 31) / 32;
+        lane = threadIdx.x & 31;
+        e = -1;
+        t0 = t1 = 0;
+        const int first = lane * per;
         int m = 0;
-        for (int i = lo; i < hi; ++i) m = max(m, tab.off[i]);
-        int before = __shfl_up_sync(0xffffffffu, m, 1);
+        for (int i = 0; i < per; ++i) m = max(m, at(first + i));
+        before = __shfl_up_sync(0xffffffffu, m, 1);
         if (lane == 0) before = 0;
+#pragma unroll
         for (int o = 1; o < 32; o <<= 1) {
             const int v = __shfl_up_sync(0xffffffffu, before, o);
             if (lane >= o) before = max(before, v);
         }
-        m = before;
-        for (int i = lo; i < hi; ++i) tab.off[i] = m = max(m, tab.off[i]);
-        __syncwarp();
-        int sum = 0;
-        for (int i = lo; i < hi && i < p.experts; ++i) sum += (tab.off[i + 1] - tab.off[i] + TILE - 1) / TILE;
-        int at = sum;
-        for (int o = 1; o < 32; o <<= 1) {
-            const int v = __shfl_up_sync(0xffffffffu, at, o);
-            if (lane >= o) at += v;
+        mine = 0;
+        int prev = max(before, at(first));
+        for (int i = 0; i < per; ++i) {  // past the last expert at() repeats the last offset: no tiles
+            const int next = max(prev, at(first + i + 1));
+            mine += count(prev, next);
+            prev = next;
         }
-        at -= sum;
-        for (int i = lo; i < hi; ++i) {
-            tab.tiles[i] = at;
-            if (i < p.experts) at += (tab.off[i + 1] - tab.off[i] + TILE - 1) / TILE;
+        tiles = mine;
+#pragma unroll
+        for (int o = 1; o < 32; o <<= 1) {
+            const int v = __shfl_up_sync(0xffffffffu, tiles, o);
+            if (lane >= o) tiles += v;
         }
     }
-    __syncthreads();
-}
 
-// Work unit u; `e` is the caller's cursor (units come in rising order).
-template <int BN, int KIND, bool SWAP>
-__device__ __forceinline__ Item item_of(const Table& tab, const ExpertParams& p, int u, int& e) {
+    __device__ __forceinline__ int total() const { return __shfl_sync(0xffffffffu, tiles, 31); }
+
+    // Offsets of the experts of lane `l`: lane j gets [v, next) of expert l * per + j.
+    __device__ __forceinline__ void group(int l, int& v, int& next) const {
+        v = max(at(l * per + min(lane, per)), __shfl_sync(0xffffffffu, before, l));
+#pragma unroll
+        for (int o = 1; o < 32; o <<= 1) {
+            const int w = __shfl_up_sync(0xffffffffu, v, o);
+            if (lane >= o) v = max(v, w);
+        }
+        next = __shfl_down_sync(0xffffffffu, v, 1);
+        if (lane >= per) next = v;
+    }
+
+    // The expert that tile t (< total) belongs to.
+    __device__ __forceinline__ void find_tile(int t) {
+        if (t >= t0 && t < t1) return;
+        const int l = __ffs(__ballot_sync(0xffffffffu, tiles > t)) - 1;
+        const int base = __shfl_sync(0xffffffffu, tiles - mine, l);
+        int v, next;
+        group(l, v, next);
+        const int n = count(v, next);
+        int sum = n;
+#pragma unroll
+        for (int o = 1; o < 32; o <<= 1) {
+            const int w = __shfl_up_sync(0xffffffffu, sum, o);
+            if (lane >= o) sum += w;
+        }
+        const int k = __ffs(__ballot_sync(0xffffffffu, base + sum > t)) - 1;
+        e = l * per + k;
+        lo = __shfl_sync(0xffffffffu, v, k);
+        hi = __shfl_sync(0xffffffffu, next, k);
+        t1 = base + __shfl_sync(0xffffffffu, sum, k);
+        t0 = t1 - __shfl_sync(0xffffffffu, n, k);
+    }
+
+    // Expert x (< experts).
+    __device__ __forceinline__ void find_expert(int x) {
+        if (x == e) return;
+        int v, next;
+        group(x / per, v, next);
+        e = x;
+        lo = __shfl_sync(0xffffffffu, v, x % per);
+        hi = __shfl_sync(0xffffffffu, next, x % per);
+    }
+};
+
+// Work unit u.
+template <int BN, int KIND, bool SWAP, int TILE>
+__device__ __forceinline__ Item item_of(Experts<TILE>& x, const ExpertParams& p, int u) {
     Item it;
     int mb, nb, b;
     if constexpr (KIND == kSumTN) {
-        const int per = p.m_tiles * p.n_tiles;
-        e = u / per;
+        const int per = p.m_tiles * p.n_tiles, e = u / per;
         tile_coords(u - e * per, TileWalk{p.m_tiles, p.n_tiles, 16}, mb, nb, b);
+        x.find_expert(e);
         it.m0 = mb * BM;
         it.m_end = p.M;
         it.n0 = nb * BN;
-        it.k_row = tab.off[e];
-        it.k_end = tab.off[e + 1];
-        it.kbs = (it.k_end - it.k_row + BK - 1) / BK;
+        it.k_row = x.lo;
+        it.k_end = x.hi;
+        it.kbs = (x.hi - x.lo + BK - 1) / BK;
     } else {
-        while (u >= tab.tiles[e + 1] * p.n_tiles) ++e;
-        const int t = u - tab.tiles[e] * p.n_tiles, mt = tab.tiles[e + 1] - tab.tiles[e];
+        x.find_tile(u / p.n_tiles);
+        const int t = u - x.t0 * p.n_tiles, mt = x.t1 - x.t0;
         if constexpr (SWAP) {
             mb = t % mt;  // the row tiles of one weight tile one after the other
             nb = t / mt;
-            it.m0 = tab.off[e] + mb * BN;
             it.n0 = nb * BM;
         } else {
             tile_coords(t, TileWalk{mt, p.n_tiles, 16}, mb, nb, b);
-            it.m0 = tab.off[e] + mb * BM;
             it.n0 = nb * BN;
         }
-        it.m_end = tab.off[e + 1];
+        it.m0 = x.lo + mb * TILE;
+        it.m_end = x.hi;
         it.k_row = it.k_end = 0;
         it.kbs = p.k_blocks;
     }
-    it.e = e;
+    it.e = x.e;
     return it;
 }
-
-template <int BN, int STAGES>
-struct ExpertSmem : Smem<BN, STAGES, 1, 3> {
-    using Base = Smem<BN, STAGES, 1, 3>;
-    static constexpr int kTableOffset = (Base::kBytes + 15) / 16 * 16;
-    static constexpr int kTotal = kTableOffset + int(sizeof(Table)) + 1024;
-    static_assert(kTotal <= 227 * 1024, "shared memory per CTA");
-};
 
 // KIND, SWAP: see the head of the file. BN: output columns of a tile, or
 // token rows of a swapped one.
 template <int BN, int KIND, int STAGES, bool SWAP>
-__global__ void __maxnreg__(168)
+__global__ void __maxnreg__(SWAP ? 168 : kActRegs)
 expert_kernel(const __grid_constant__ CUtensorMap tm_a, const __grid_constant__ CUtensorMap tm_b,
               const __grid_constant__ CUtensorMap tm_c, const __grid_constant__ CUtensorMap tm_z, const ExpertParams p) {
-    using L = ExpertSmem<BN, STAGES>;
+    using L = Smem<BN, STAGES, 1, SWAP ? 3 : 4>;
+    constexpr int ET = epi_threads(true, SWAP);
+    constexpr int TILE = SWAP ? BN : BM;
     // majors of the MMA's operands: K-major unless the stored rows run along K
     constexpr bool A_MN = SWAP ? KIND == kRowsNN : KIND == kSumTN;
     constexpr bool B_MN = !SWAP && KIND != kRowsNT;
@@ -172,7 +222,6 @@ expert_kernel(const __grid_constant__ CUtensorMap tm_a, const __grid_constant__ 
     const uint32_t bar_tempty = bar_tfull + 2 * 8;
     uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(smem + L::kBarOffset + (2 * STAGES + 4) * 8);
     float* s_bias = reinterpret_cast<float*>(smem + L::kBiasOffset);
-    Table& tab = *reinterpret_cast<Table*>(smem + L::kTableOffset);
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
 
     if (warp == 0 && lane == 0) {
@@ -182,7 +231,7 @@ expert_kernel(const __grid_constant__ CUtensorMap tm_a, const __grid_constant__ 
         }
         for (int b = 0; b < 2; ++b) {
             mbar_init(bar_tfull + 8 * b, 1);
-            mbar_init(bar_tempty + 8 * b, kEpiThreads);
+            mbar_init(bar_tempty + 8 * b, ET);
         }
         fence_mbar_init();
         tma_prefetch(&tm_a);
@@ -196,22 +245,24 @@ expert_kernel(const __grid_constant__ CUtensorMap tm_a, const __grid_constant__ 
         tmem_alloc<1>(smem_addr(tmem_slot), L::kTmemCols);
         tmem_relinquish<1>();
     }
-    griddep_wait();  // the offsets are read next
-    griddep_launch();
     tc_fence_before();
-    build_table<SWAP ? BN : BM>(tab, p);  // ends with a block barrier
+    __syncthreads();
     tc_fence_after();
     const uint32_t tmem_base = *tmem_slot;
-    const int units = KIND == kSumTN ? p.experts * p.m_tiles * p.n_tiles : tab.tiles[p.experts] * p.n_tiles;
+    griddep_wait();
+    griddep_launch();
+    Experts<TILE> x;
+    x.init(p);
+    const int units = KIND == kSumTN ? p.experts * p.m_tiles * p.n_tiles : x.total() * p.n_tiles;
 
     if (warp == 0) {
         // ------------------------------------------------ TMA producer ---
         const bool issuer = elect_one();
-        int stage = 0, e = 0;
+        int stage = 0;
         uint32_t phase = 0;
         bool ok = true;
         for (int u = blockIdx.x; u < units && ok; u += gridDim.x) {
-            const Item it = item_of<BN, KIND, SWAP>(tab, p, u, e);
+            const Item it = item_of<BN, KIND, SWAP>(x, p, u);
             for (int kb = 0; kb < it.kbs; ++kb) {
                 if (!wait_bounded_warp(bar_empty + 8 * stage, phase ^ 1)) { ok = false; break; }
                 const uint32_t full = bar_full + 8 * stage;
@@ -254,11 +305,11 @@ expert_kernel(const __grid_constant__ CUtensorMap tm_a, const __grid_constant__ 
         const bool issuer = elect_one();
         const uint64_t a_desc0 = A_MN ? smem_desc_sw128(s_a, 128 * BK, 1024) : smem_desc_sw128(s_a, 16, 1024);
         const uint64_t b_desc0 = B_MN ? smem_desc_sw128(s_b, 128 * BK, 1024) : smem_desc_sw128(s_b, 16, 1024);
-        int stage = 0, e = 0, done = 0;
+        int stage = 0, done = 0;
         uint32_t phase = 0;
         bool ok = true;
         for (int u = blockIdx.x; u < units && ok; u += gridDim.x) {
-            const Item it = item_of<BN, KIND, SWAP>(tab, p, u, e);
+            const Item it = item_of<BN, KIND, SWAP>(x, p, u);
             if (it.kbs == 0) continue;  // an expert without rows: the epilogue writes its zeros
             const int buf = done & 1;
             if (!wait_bounded_warp(bar_tempty + 8 * buf, ((done >> 1) & 1) ^ 1)) break;
@@ -283,31 +334,38 @@ expert_kernel(const __grid_constant__ CUtensorMap tm_a, const __grid_constant__ 
         const int q = warp & 3;  // TMEM lane quarter this warp may access
         const int row_in_tile = q * 32 + lane;
         const int etid = threadIdx.x - 64;
-        const bool store_lead = etid == 0;
+        const int phase = (warp - 2) >> 2;
         const uint32_t stg0 = s_a + L::kStgOffset;
         const float inv_a = 1.0f / __ldg(p.sa);
-        int n_st = 0, e = 0, done = 0;
+        int done = 0;
+        float unused = 0.0f;
+        ActResidual none;
         bool failed = false;
+        if constexpr (KIND == kSumTN) {  // no bias
+            for (int j = etid; j < BN; j += ET) s_bias[j] = 0.0f;
+            epilogue_bar<ET>();
+        }
         for (int u = blockIdx.x; u < units; u += gridDim.x) {
-            const Item it = item_of<BN, KIND, SWAP>(tab, p, u, e);
+            const Item it = item_of<BN, KIND, SWAP>(x, p, u);
             const float inv = inv_a * (1.0f / __ldg(p.sb + int64_t(it.e) * p.sb_stride));
             const bool has = it.kbs > 0;
             const int buf = done & 1;
+            float bias_v = 0.0f;  // of column etid
             if constexpr (!SWAP && KIND != kSumTN) {
-                epilogue_bar();  // the previous tile's readers are done
-                for (int j = etid; j < BN; j += kEpiThreads) {
-                    const int col = it.n0 + j;
-                    s_bias[j] = (p.bias && col < p.N) ? bf16_value(__ldg(p.bias + int64_t(it.e) * p.N + col)) : 0.0f;
-                }
-                epilogue_bar();
+                const int col = it.n0 + etid;
+                if (p.bias && etid < BN && col < p.N) bias_v = bf16_value(__ldg(p.bias + int64_t(it.e) * p.N + col));
             }
             float bias_row = 0.0f;
             if (SWAP && p.bias && it.n0 + row_in_tile < p.N)
                 bias_row = bf16_value(__ldg(p.bias + int64_t(it.e) * p.N + it.n0 + row_in_tile));
             if (has) {
                 if (!failed) failed = !wait_bounded(bar_tfull + 8 * buf, (done >> 1) & 1);
-                failed = epilogue_bar_or(failed);
+                failed = epilogue_bar_or<ET>(failed);  // the previous tile's readers are done, too
                 if (failed) continue;
+                if constexpr (!SWAP && KIND != kSumTN) {
+                    if (etid < BN) s_bias[etid] = bias_v;
+                    epilogue_bar<ET>();
+                }
                 tc_fence_after();
             }
             const uint32_t t_row = tmem_base + (uint32_t(q * 32) << 16) + buf * BN;
@@ -338,75 +396,32 @@ expert_kernel(const __grid_constant__ CUtensorMap tm_a, const __grid_constant__ 
                     }
                 }
             } else {
-                const int row = it.m0 + row_in_tile;
-                uint16_t* out = KIND == kSumTN ? p.out + int64_t(it.e) * p.M * p.N : p.out;
-                const int left = (p.N - it.n0 + 31) / 32;
-                const int nch = left < BN / 32 ? left : BN / 32;
-                const bool whole = p.fast && (KIND == kSumTN || it.m0 + BM <= it.m_end);
-                // one 128 x 32 block to global memory
-                auto put = [&](const float (&y)[32], uint16_t* dst, const CUtensorMap* map, int col0) {
-                    if (whole) {
-                        stage_and_store<L>(stg0, n_st, row_in_tile, y, store_lead, map, col0, it.m0,
-                                           KIND == kSumTN ? it.e : 0);
-                        ++n_st;
-                    } else if (p.fast) {
-                        // an expert's last rows: staged by the warp for itself, then 64-byte row pieces
-                        const uint32_t stg = stg0 + uint32_t(n_st % L::kStgBufs) * L::kStgBytes;
-#pragma unroll
-                        for (int j = 0; j < 4; ++j)
-                            asm volatile("st.shared.v4.b32 [%0], {%1, %2, %3, %4};" ::"r"(
-                                             stg + row_in_tile * 64 + ((j ^ ((row_in_tile >> 1) & 3)) << 4)),
-                                         "r"(pack_bf16x2(y[8 * j + 0], y[8 * j + 1])),
-                                         "r"(pack_bf16x2(y[8 * j + 2], y[8 * j + 3])),
-                                         "r"(pack_bf16x2(y[8 * j + 4], y[8 * j + 5])),
-                                         "r"(pack_bf16x2(y[8 * j + 6], y[8 * j + 7]))
-                                         : "memory");
-                        __syncwarp();
-                        const int piece = lane & 3, col = col0 + piece * 8;
-#pragma unroll
-                        for (int j = 0; j < 4; ++j) {
-                            const int r = q * 32 + (lane >> 2) + 8 * j;
-                            uint4 w;
-                            asm volatile("ld.shared.v4.b32 {%0, %1, %2, %3}, [%4];"
-                                         : "=r"(w.x), "=r"(w.y), "=r"(w.z), "=r"(w.w)
-                                         : "r"(stg + r * 64 + ((piece ^ ((r >> 1) & 3)) << 4))
-                                         : "memory");
-                            if (it.m0 + r < it.m_end && col < p.N)
-                                *reinterpret_cast<uint4*>(dst + int64_t(it.m0 + r) * p.N + col) = w;
-                        }
-                        // every TMA store has read its tile before the next block is staged: this
-                        // block issues none, so a store three back could be the newest one pending
-                        if (store_lead) bulk_wait_read<0>();
-                        epilogue_bar();
-                        ++n_st;
-                    } else if (row < it.m_end) {
-#pragma unroll
-                        for (int i = 0; i < 32; ++i)
-                            if (col0 + i < p.N) dst[int64_t(row) * p.N + col0 + i] = bf16_bits(y[i]);
-                    }
-                };
-#pragma unroll 1
-                for (int c = 0; c < nch; ++c) {
-                    const int col0 = it.n0 + c * 32;
-                    float y[32];
-                    if (has) {
-                        uint32_t r[32];
-                        __syncwarp();
-                        tmem_ld<32>(t_row + c * 32, r);
-                        tmem_ld_wait();
-#pragma unroll
-                        for (int i = 0; i < 32; ++i)
-                            y[i] = KIND == kSumTN ? __uint_as_float(r[i]) * inv
-                                                  : fmaf(__uint_as_float(r[i]), inv, s_bias[c * 32 + i]);
-                    } else {
-#pragma unroll
-                        for (int i = 0; i < 32; ++i) y[i] = 0.0f;
-                    }
-                    if constexpr (KIND != kSumTN) {
-                        if (p.preact) put(y, p.preact, &tm_z, col0);
-                        act_apply(p.act, y);
-                    }
-                    put(y, out, &tm_c, col0);
+                ActTile t;
+                t.map_out = &tm_c;
+                t.map_z = &tm_z;
+                t.out = KIND == kSumTN ? p.out + int64_t(it.e) * p.M * p.N : p.out;
+                t.preact = p.preact;
+                t.residual = nullptr;
+                t.s_bias = s_bias;
+                t.t_row = t_row;
+                t.stg = stg0 + uint32_t(warp - 2) * 2048u;
+                t.inv = inv;
+                t.s_out = 1.0f;
+                t.act = p.act;
+                t.out_fmt = 0;
+                t.row0 = it.m0 + q * 32;
+                t.m_end = it.m_end;
+                t.col_first = it.n0;
+                t.N = p.N;
+                t.b = KIND == kSumTN ? it.e : 0;
+                // a warp whose rows end inside its 32 writes them row by row
+                t.tma_out = t.tma_z = p.fast && (KIND == kSumTN || t.row0 + 32 <= it.m_end);
+                t.vec_out = t.vec_z = p.fast;
+                t.has = has;
+                if constexpr (KIND == kSumTN) {
+                    if (t.row0 < t.m_end) act_blocks<BN, FP8_ACT_NONE, false>(t, none, unused, phase, lane);
+                } else {
+                    act_tile<BN, false>(t, none, unused, phase, lane);
                 }
             }
             if (has) {
@@ -415,7 +430,7 @@ expert_kernel(const __grid_constant__ CUtensorMap tm_a, const __grid_constant__ 
                 ++done;
             }
         }
-        if (store_lead) bulk_wait_read<0>();  // the staging tiles outlive the stores that read them
+        if (!SWAP && lane == 0) bulk_wait_read<0>();  // the staging tiles outlive the stores that read them
     }
 
     tc_fence_before();
@@ -444,20 +459,20 @@ bool make_block_map(CUtensorMap* map, const void* base, uint64_t cols, uint64_t 
 template <int BN, int KIND, int STAGES, bool SWAP>
 fp8_status launch_experts(const CUtensorMap& ta, const CUtensorMap& tb, const CUtensorMap& tc, const CUtensorMap& tz,
                           ExpertParams p, int fa, int fb, int64_t most_units, cudaStream_t st) {
-    using L = ExpertSmem<BN, STAGES>;
+    using L = Smem<BN, STAGES, 1, SWAP ? 3 : 4>;
     auto kern = expert_kernel<BN, KIND, STAGES, SWAP>;
     static bool attr_set[64] = {false};
     int dev = 0;
     if (cudaGetDevice(&dev) != cudaSuccess || dev < 0 || dev >= 64) return FP8_ERR_CUDA;
     if (!attr_set[dev]) {
-        if (cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, L::kTotal) != cudaSuccess)
+        if (cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, L::kAlloc) != cudaSuccess)
             return FP8_ERR_CUDA;
         attr_set[dev] = true;
     }
     p.idesc = SWAP ? instr_desc_f8(fb, fa, KIND == kRowsNN, 0, BM, BN)
                    : instr_desc_f8(fa, fb, KIND == kSumTN, KIND != kRowsNT, BM, BN);
     const int grid = int(most_units < sm_count() ? most_units : sm_count());
-    return launch_pdl(kern, grid, kThreads, L::kTotal, st, 1, ta, tb, tc, tz, p);
+    return launch_pdl(kern, grid, 64 + epi_threads(true, SWAP), L::kAlloc, st, 1, ta, tb, tc, tz, p);
 }
 
 }  // namespace
@@ -516,7 +531,7 @@ extern "C" fp8_status fp8_mm_experts(const uint8_t* a8, fp8_fmt fa, const uint8_
         const int64_t units = int64_t(experts) * p.m_tiles * p.n_tiles;
         if (units >= kMost) return FP8_ERR_UNSUPPORTED;
         if (!make_block_map(&ta, a8, M, rows) || !make_block_map(&tb, b8, N, rows)) return FP8_ERR_CUDA;
-        if (p.fast && !make_out_map(&tc, out, N, M, experts, uint64_t(M) * N * 2)) return FP8_ERR_CUDA;
+        if (p.fast && !make_out_map(&tc, out, N, M, experts, uint64_t(M) * N * 2, 32)) return FP8_ERR_CUDA;
         return launch_experts<BN, kSumTN, 4, false>(ta, tb, tc, tz, p, fa, fb, units, st);
     }
     const bool nn = layout == FP8_NN;
@@ -544,8 +559,8 @@ extern "C" fp8_status fp8_mm_experts(const uint8_t* a8, fp8_fmt fa, const uint8_
                     (nn ? make_map(&tb, b8, N, K, experts, uint64_t(N) * K, 128, BK)
                         : make_map(&tb, b8, K, N, experts, uint64_t(N) * K, BK, BN));
     if (!ok) return FP8_ERR_CUDA;
-    if (p.fast && !make_out_map(&tc, out, N, rows, 1, 0)) return FP8_ERR_CUDA;
-    if (p.fast && preact && !make_out_map(&tz, preact, N, rows, 1, 0)) return FP8_ERR_CUDA;
+    if (p.fast && !make_out_map(&tc, out, N, rows, 1, 0, 32)) return FP8_ERR_CUDA;
+    if (p.fast && preact && !make_out_map(&tz, preact, N, rows, 1, 0, 32)) return FP8_ERR_CUDA;
     return nn ? launch_experts<BN, kRowsNN, 4, false>(ta, tb, tc, tz, p, fa, fb, units, st)
               : launch_experts<BN, kRowsNT, 4, false>(ta, tb, tc, tz, p, fa, fb, units, st);
 }

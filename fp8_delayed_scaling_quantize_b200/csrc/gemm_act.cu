@@ -1,5 +1,5 @@
 // FP8 GEMM with an activation and a residual in its epilogue: the kernel of
-// gemm_kernel.cuh with its EP epilogue (epilogue_act, and the swapped one).
+// gemm_kernel.cuh with its EP epilogue (act_tile, and the swapped one).
 //
 //   z = acc / (sa sb) + bias;  out = bf16(act(z) + residual), preact = bf16(z)
 //
@@ -67,7 +67,7 @@ fp8_status mm_act_impl(const uint8_t* a8, fp8_fmt fa, const uint8_t* b8, fp8_fmt
         p.out_ring = o.ring;
         p.out_amax = o.amax;
         p.out_scale = o.scale;
-        p.vec_store = N % 16 == 0 && stride_c % 16 == 0 && aligned(out, 16);
+        p.tma_store = N % 16 == 0 && stride_c % 16 == 0 && aligned(out, 16);
     }
     EpArgs<true> ep = {};
     ep.act = o.act;
@@ -82,8 +82,8 @@ fp8_status mm_act_impl(const uint8_t* a8, fp8_fmt fa, const uint8_t* b8, fp8_fmt
                                                              nullptr, 0, 0, st, ep);
     ep.fast = N % 8 == 0 && stride_c % 8 == 0 && (o.out8 || aligned(out, 16)) &&
               (!o.residual || (ep.stride_r % 8 == 0 && aligned(o.residual, 16))) && aligned(o.preact, 16);
-    p.tma_store = !o.out8 && ep.fast;
-    if (ep.fast && o.preact && !make_out_map(&ep.tz, o.preact, N, M, batch, uint64_t(stride_c) * 2)) return FP8_ERR_CUDA;
+    if (!o.out8) p.tma_store = ep.fast;
+    if (ep.fast && o.preact && !make_out_map(&ep.tz, o.preact, N, M, batch, uint64_t(stride_c) * 2, 32)) return FP8_ERR_CUDA;
 
     CUtensorMap ta;
     const bool a_mn = layout == FP8_TN;

@@ -71,6 +71,10 @@ constexpr int BM = 128;
 constexpr int BK = 128;  // bytes = elements of K per stage
 constexpr int kEpiThreads = 128;            // 4 epilogue warps, one per TMEM lane quarter
 constexpr int kThreads = 64 + kEpiThreads;  // producer warp, MMA warp, epilogue
+// An activation epilogue on unswapped tiles runs sixteen warps (at 96
+// registers a thread: the file serves a block in steps of four warps, 20 here).
+__host__ __device__ constexpr int epi_threads(bool ep, bool swap) { return ep && !swap ? 4 * kEpiThreads : kEpiThreads; }
+constexpr int kActRegs = 96;
 constexpr uint64_t kWaitLimitNs = 2000000000ull;  // 2 s per wait
 
 struct GemmParams {
@@ -280,8 +284,8 @@ struct Smem {
     // three 128-row x 32-column bf16 staging tiles (64-byte swizzle), used in
     // turn, so that a chunk waits only for the store two chunks back; 24 KB
     // in all, so that a waiting kernel's small blocks still fit on the SM
-    // beside this CTA. An activation epilogue takes four: its residual is
-    // written into the tile after the next, which must be free as early
+    // beside this CTA. An activation epilogue takes four: 2 KB for each of its
+    // sixteen warps
     static constexpr int kStgBufs = STG;
     static constexpr int kStgPending = 1;  // stores that may still be reading their tile when one more is issued
     static_assert(STG >= 3, "");
@@ -330,9 +334,13 @@ __device__ __forceinline__ T pin(T v) {
 }
 
 // Named barrier 1: the epilogue warps.
-__device__ __forceinline__ void epilogue_bar() { asm volatile("bar.sync 1, %0;" ::"n"(kEpiThreads) : "memory"); }
+template <int T = kEpiThreads>
+__device__ __forceinline__ void epilogue_bar() {
+    asm volatile("bar.sync 1, %0;" ::"n"(T) : "memory");
+}
 
 // Barrier 1, returning whether any epilogue thread passed true.
+template <int T = kEpiThreads>
 __device__ __forceinline__ bool epilogue_bar_or(bool v) {
     uint32_t r;
     asm volatile(
@@ -341,7 +349,7 @@ __device__ __forceinline__ bool epilogue_bar_or(bool v) {
         "bar.red.or.pred p, 1, %2, q;\n\t"
         "selp.u32 %0, 1, 0, p;\n\t}"
         : "=r"(r)
-        : "r"(uint32_t(v)), "n"(kEpiThreads)
+        : "r"(uint32_t(v)), "n"(T)
         : "memory");
     return r != 0;
 }
@@ -376,128 +384,224 @@ __device__ __forceinline__ void stage_and_store(uint32_t stg0, int n_st, int row
     }
 }
 
-// The epilogue of one 128 x BN tile through an activation (unswapped tiles).
-// Per 32 columns: z = acc * inv + bias, kept as bf16 if asked for, then
-// act(z) + residual as bf16, or act(z) as FP8 codes under the output ring's
-// scale. A fast launch stages every bf16 block for a TMA store; its residual
-// arrives as 64-byte row pieces (a warp's load covers 8 rows), one block
-// ahead, and passes through the staging tile that the output block will take,
-// so that each thread finds its own row there. Only this warp's rows are
-// exchanged, and the thread that reads a row is the one that overwrites it.
-template <int BN, bool OUT8, typename L>
-__device__ __forceinline__ void epilogue_act(const GemmParams& p, const EpArgs<true>& ep, const CUtensorMap* map_c,
-                                             uint32_t t_row, const float* s_bias, uint32_t stg0, int& n_st, int q,
-                                             int lane, bool store_lead, float inv, float s_out, float& m_out, int m0,
-                                             int col_first, int b, int M, int N, bool vec_store) {
-    const int row_in_tile = q * 32 + lane;
-    const int row = m0 + row_in_tile;
-    const int left = (N - col_first + 31) / 32;
-    const int nch = left < BN / 32 ? left : BN / 32;
-    const bool has_z = ep.preact != nullptr, has_r = !OUT8 && ep.residual != nullptr;
-    const int64_t at = int64_t(b) * p.stride_c + int64_t(row) * N;  // this row in out and preact
-    const uint16_t* res = has_r ? ep.residual + int64_t(b) * ep.stride_r : nullptr;
-    const int piece = lane & 3, prow = q * 32 + (lane >> 2);  // residual pieces: rows prow + 8 j
-    uint4 rp[4];
-    auto load_residual = [&](int c) {
-        const int col = col_first + c * 32 + piece * 8;
+// One output tile of an activation epilogue (unswapped), as one of its warps
+// sees it. Rows below m_end and columns below N exist; `out`, `preact` and
+// `residual` point at the row 0 and column 0 that row0 and col_first count
+// from.
+struct ActTile {
+    const CUtensorMap* map_out;
+    const CUtensorMap* map_z;
+    void* out;                 // bf16, or codes
+    uint16_t* preact;          // or NULL
+    const uint16_t* residual;  // or NULL; may be out
+    const float* s_bias;       // the tile's bias, in shared memory
+    uint32_t t_row;            // accumulator: this warp's lanes, the tile's first column
+    uint32_t stg;              // this warp's staging tile (2 KB)
+    float inv, s_out;
+    int act, out_fmt;
+    int row0, m_end;  // this warp's first row
+    int col_first, N, b;
+    bool tma_out, tma_z;  // blocks of 32 rows leave by TMA
+    bool vec_out, vec_z;  // else: 16-byte pieces of rows may be written (vec_z: preact, and residual read)
+    bool has;             // there is an accumulator (else the products are 0)
+};
+
+// 16-byte piece j of row r of a 32-row staging tile of bf16 (64-byte swizzle)
+// and of codes (32-byte swizzle): the lanes of a phase hit distinct banks.
+__device__ __forceinline__ uint32_t stg_bf16(uint32_t stg, int r, int j) { return stg + r * 64 + ((j ^ ((r >> 1) & 3)) << 4); }
+__device__ __forceinline__ uint32_t stg_code(uint32_t stg, int r, int j) { return stg + r * 32 + ((j ^ ((r >> 2) & 1)) << 4); }
+
+__device__ __forceinline__ void sts128(uint32_t a, uint32_t x, uint32_t y, uint32_t z, uint32_t w) {
+    asm volatile("st.shared.v4.b32 [%0], {%1, %2, %3, %4};" ::"r"(a), "r"(x), "r"(y), "r"(z), "r"(w) : "memory");
+}
+__device__ __forceinline__ uint4 lds128(uint32_t a) {
+    uint4 v;
+    asm volatile("ld.shared.v4.b32 {%0, %1, %2, %3}, [%4];" : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w) : "r"(a) : "memory");
+    return v;
+}
+
+// The warp's staging tile is free again: the TMA store of it, if any, has read it.
+__device__ __forceinline__ void act_stage_free(int lane) {
+    if (lane == 0) bulk_wait_read<0>();
+    __syncwarp();
+}
+
+// The staged block to global memory: by TMA, which clips what the map does
+// not hold, or row by row as far as rows and columns exist. PIECES: 16-byte
+// pieces of a staged row (4 for bf16, 2 for codes).
+template <int PIECES>
+__device__ __forceinline__ void act_store(const ActTile& t, void* dst, const CUtensorMap* map, bool tma, bool vec,
+                                          int col0, int lane) {
+    constexpr int kElem = PIECES / 2;  // bytes of a value
+    auto slot = [&](int r, int j) { return PIECES == 4 ? stg_bf16(t.stg, r, j) : stg_code(t.stg, r, j); };
+    uint8_t* d = static_cast<uint8_t*>(dst);
+    if (tma) {
+        fence_proxy_async_smem();
+        __syncwarp();
+        if (lane == 0) {
+            tma_store_3d(map, t.stg, col0, t.row0, t.b);
+            bulk_commit();
+        }
+    } else if (vec) {
+        __syncwarp();
+        const int piece = lane % PIECES, col = col0 + piece * (16 / kElem);
+#pragma unroll
+        for (int r = lane / PIECES; r < 32; r += 32 / PIECES) {
+            const uint4 w = lds128(slot(r, piece));
+            if (t.row0 + r < t.m_end && col < t.N)
+                *reinterpret_cast<uint4*>(d + (int64_t(t.row0 + r) * t.N + col) * kElem) = w;
+        }
+    } else {
+        __syncwarp();
+        const int at = lane * kElem;  // byte of a staged row: one column a lane
+#pragma unroll 1
+        for (int r = 0; r < 32 && t.row0 + r < t.m_end; ++r) {
+            const uint32_t addr = slot(r, at >> 4) + (at & 15);
+            uint16_t v;
+            if (kElem == 2) asm volatile("ld.shared.u16 %0, [%1];" : "=h"(v) : "r"(addr) : "memory");
+            else            asm volatile("{\n\t.reg .b32 w;\n\tld.shared.u8 w, [%1];\n\tcvt.u16.u32 %0, w;\n\t}" : "=h"(v) : "r"(addr) : "memory");
+            if (col0 + lane < t.N) {
+                const int64_t o = int64_t(t.row0 + r) * t.N + col0 + lane;
+                if (kElem == 2) reinterpret_cast<uint16_t*>(d)[o] = v;
+                else            d[o] = uint8_t(v);
+            }
+        }
+    }
+}
+
+__device__ __forceinline__ void act_stage(uint32_t stg, const float (&y)[32], int lane) {
+#pragma unroll
+    for (int j = 0; j < 4; ++j)
+        sts128(stg_bf16(stg, lane, j), pack_bf16x2(y[8 * j + 0], y[8 * j + 1]), pack_bf16x2(y[8 * j + 2], y[8 * j + 3]),
+               pack_bf16x2(y[8 * j + 4], y[8 * j + 5]), pack_bf16x2(y[8 * j + 6], y[8 * j + 7]));
+}
+
+// A warp's part of an activation epilogue: its 32 rows of the tile, every
+// fourth block of 32 columns. Sixteen warps share a tile (four to a TMEM lane
+// quarter and to a scheduler), because the epilogue is bound by latency: a
+// block is a chain of TMEM load, MUFU, staging and store, which one warp a
+// scheduler left bare. Each warp stages and stores its own blocks, so that the
+// warps drift apart and overlap; only the bias and the accumulator hand-over
+// bring them together. Per block: z = acc * inv + bias, kept as bf16 if asked
+// for, then act(z) + residual as bf16, or act(z) as FP8 codes under the output
+// ring's scale (m_out: their amax so far). The residual arrives as 64-byte row
+// pieces (a warp's load covers 8 rows), the first block's before the
+// accumulator is there, and passes through the staging tile, where each
+// thread finds its own row.
+constexpr int kActPhases = 4;
+
+struct ActResidual {
+    uint4 v[4];
+    // rows (lane / 4) + 8 j of block c, 16-byte piece lane % 4
+    __device__ __forceinline__ void load(const ActTile& t, int c, int lane) {
+        const int col = t.col_first + c * 32 + (lane & 3) * 8;
 #pragma unroll
         for (int j = 0; j < 4; ++j) {
-            const int r = m0 + prow + 8 * j;
-            rp[j] = (r < M && col < N) ? __ldcg(reinterpret_cast<const uint4*>(res + int64_t(r) * N + col))
-                                       : make_uint4(0, 0, 0, 0);
+            const int r = t.row0 + (lane >> 2) + 8 * j;
+            v[j] = (r < t.m_end && col < t.N)
+                       ? __ldcg(reinterpret_cast<const uint4*>(t.residual + int64_t(r) * t.N + col))
+                       : make_uint4(0, 0, 0, 0);
         }
-    };
-    auto process = [&](const uint32_t (&acc)[32], int c) {
-        const int col0 = col_first + c * 32;
+    }
+};
+
+template <int BN, int ACT, bool OUT8>
+__device__ __forceinline__ void act_blocks(const ActTile& t, ActResidual& res, float& m_out, int phase, int lane) {
+    const int left = (t.N - t.col_first + 31) / 32;
+    const int nch = left < BN / 32 ? left : BN / 32;
+#pragma unroll 1
+    for (int c = phase; c < nch; c += kActPhases) {
+        const int col0 = t.col_first + c * 32;
+        uint32_t acc[32];
+        if (t.has) {
+            __syncwarp();
+            tmem_ld<32>(t.t_row + c * 32, acc);
+            tmem_ld_wait_tied(acc);
+        } else {
+#pragma unroll
+            for (int i = 0; i < 32; ++i) acc[i] = 0u;
+        }
         float y[32];
 #pragma unroll
-        for (int i = 0; i < 32; ++i) y[i] = fmaf(__uint_as_float(acc[i]), inv, s_bias[c * 32 + i]);
-        if (ep.fast) {
-            if (has_r) {
-                const uint32_t stg = stg0 + uint32_t((n_st + has_z) % L::kStgBufs) * L::kStgBytes;
+        for (int i = 0; i < 32; i += 4) {
+            const float4 bias = *reinterpret_cast<const float4*>(t.s_bias + c * 32 + i);
+            split(fma2(f2(__uint_as_float(acc[i]), __uint_as_float(acc[i + 1])), f2(t.inv), f2(bias.x, bias.y)), y[i],
+                  y[i + 1]);
+            split(fma2(f2(__uint_as_float(acc[i + 2]), __uint_as_float(acc[i + 3])), f2(t.inv), f2(bias.z, bias.w)),
+                  y[i + 2], y[i + 3]);
+        }
+        if (t.preact) {
+            act_stage_free(lane);
+            act_stage(t.stg, y, lane);
+            act_store<4>(t, t.preact, t.map_z, t.tma_z, t.vec_z, col0, lane);
+        }
+        if (ACT != FP8_ACT_NONE) act_each<ACT>(y);
+        if (!OUT8 && t.residual) {
+            act_stage_free(lane);
+            if (t.vec_z) {
 #pragma unroll
-                for (int j = 0; j < 4; ++j) {
-                    const int r = prow + 8 * j;
-                    asm volatile("st.shared.v4.b32 [%0], {%1, %2, %3, %4};" ::"r"(stg + r * 64 +
-                                                                                  ((piece ^ ((r >> 1) & 3)) << 4)),
-                                 "r"(rp[j].x), "r"(rp[j].y), "r"(rp[j].z), "r"(rp[j].w)
+                for (int j = 0; j < 4; ++j)
+                    sts128(stg_bf16(t.stg, (lane >> 2) + 8 * j, lane & 3), res.v[j].x, res.v[j].y, res.v[j].z, res.v[j].w);
+                if (c + kActPhases < nch) res.load(t, c + kActPhases, lane);
+            } else {
+#pragma unroll 1
+                for (int r = 0; r < 32; ++r) {
+                    const bool in = t.row0 + r < t.m_end && col0 + lane < t.N;
+                    const uint16_t v = in ? t.residual[int64_t(t.row0 + r) * t.N + col0 + lane] : uint16_t(0);
+                    asm volatile("st.shared.u16 [%0], %1;" ::"r"(stg_bf16(t.stg, r, lane >> 3) + (lane & 7) * 2), "h"(v)
                                  : "memory");
                 }
-                __syncwarp();
-                if (c + 1 < nch) load_residual(c + 1);
             }
-            if (has_z) {
-                stage_and_store<L>(stg0, n_st, row_in_tile, y, store_lead, &ep.tz, col0, m0, b);
-                ++n_st;
-            }
-            act_apply(ep.act, y);
-            if (has_r) {
-                const uint32_t stg = stg0 + uint32_t(n_st % L::kStgBufs) * L::kStgBytes;
+            __syncwarp();
 #pragma unroll
-                for (int j = 0; j < 4; ++j) {
-                    uint32_t w[4];
-                    asm volatile("ld.shared.v4.b32 {%0, %1, %2, %3}, [%4];"
-                                 : "=r"(w[0]), "=r"(w[1]), "=r"(w[2]), "=r"(w[3])
-                                 : "r"(stg + row_in_tile * 64 + ((j ^ ((row_in_tile >> 1) & 3)) << 4))
-                                 : "memory");
+            for (int j = 0; j < 4; ++j) {
+                const uint4 w = lds128(stg_bf16(t.stg, lane, j));
+                const uint32_t x[4] = {w.x, w.y, w.z, w.w};
 #pragma unroll
-                    for (int k = 0; k < 4; ++k) {
-                        y[8 * j + 2 * k] += __uint_as_float(w[k] << 16);
-                        y[8 * j + 2 * k + 1] += __uint_as_float(w[k] & 0xFFFF0000u);
-                    }
-                }
-            }
-        } else {
-            if (has_z && row < M) {
-#pragma unroll
-                for (int i = 0; i < 32; ++i)
-                    if (col0 + i < N) ep.preact[at + col0 + i] = bf16_bits(y[i]);
-            }
-            act_apply(ep.act, y);
-            if (has_r && row < M) {
-#pragma unroll
-                for (int i = 0; i < 32; ++i)
-                    if (col0 + i < N) y[i] += bf16_value(res[int64_t(row) * N + col0 + i]);
+                for (int k = 0; k < 4; ++k)
+                    split(add2(f2(y[8 * j + 2 * k], y[8 * j + 2 * k + 1]),
+                               f2(__uint_as_float(x[k] << 16), __uint_as_float(x[k] & 0xFFFF0000u))),
+                          y[8 * j + 2 * k], y[8 * j + 2 * k + 1]);
             }
         }
         if constexpr (OUT8) {
-            if (row < M) {
-                uint32_t w[8];
+            const bool row_in = t.row0 + lane < t.m_end;
+            uint32_t w[8];
 #pragma unroll
-                for (int j = 0; j < 8; ++j) {
+            for (int j = 0; j < 8; ++j) {
+                uint32_t h[2];
 #pragma unroll
-                    for (int k = 0; k < 4; ++k)
-                        if (col0 + 4 * j + k < N) m_out = fmaxf(m_out, fabsf(y[4 * j + k]));
-                    w[j] = cvt_fp8x2(p.out_fmt, __fmul_rn(y[4 * j], s_out), __fmul_rn(y[4 * j + 1], s_out)) |
-                           (cvt_fp8x2(p.out_fmt, __fmul_rn(y[4 * j + 2], s_out), __fmul_rn(y[4 * j + 3], s_out)) << 16);
+                for (int k = 0; k < 4; k += 2) {
+                    const float v0 = y[4 * j + k], v1 = y[4 * j + k + 1];
+                    // columns past N hold bias 0 and products of zeros: act(0) = 0 does not raise the amax
+                    if (row_in) asm("max.abs.f32 %0, %0, %1, %2;" : "+f"(m_out) : "f"(v0), "f"(v1));
+                    float q0, q1;
+                    split(mul2(f2(v0, v1), f2(t.s_out)), q0, q1);
+                    h[k / 2] = cvt_fp8x2(t.out_fmt, q0, q1);
                 }
-                uint8_t* dst = reinterpret_cast<uint8_t*>(p.out) + at + col0;
-                if (vec_store && col0 + 32 <= N) {
-                    reinterpret_cast<uint4*>(dst)[0] = make_uint4(w[0], w[1], w[2], w[3]);
-                    reinterpret_cast<uint4*>(dst)[1] = make_uint4(w[4], w[5], w[6], w[7]);
-                } else {
-#pragma unroll
-                    for (int i = 0; i < 32; ++i)
-                        if (col0 + i < N) dst[i] = uint8_t(w[i >> 2] >> (8 * (i & 3)));
-                }
+                w[j] = h[0] | (h[1] << 16);
             }
-        } else if (ep.fast) {
-            stage_and_store<L>(stg0, n_st, row_in_tile, y, store_lead, map_c, col0, m0, b);
-            ++n_st;
-        } else if (row < M) {
-#pragma unroll
-            for (int i = 0; i < 32; ++i)
-                if (col0 + i < N) p.out[at + col0 + i] = bf16_bits(y[i]);
+            act_stage_free(lane);
+            sts128(stg_code(t.stg, lane, 0), w[0], w[1], w[2], w[3]);
+            sts128(stg_code(t.stg, lane, 1), w[4], w[5], w[6], w[7]);
+            act_store<2>(t, t.out, t.map_out, t.tma_out, t.vec_out, col0, lane);
+        } else {
+            if (!t.residual) act_stage_free(lane);
+            act_stage(t.stg, y, lane);
+            act_store<4>(t, t.out, t.map_out, t.tma_out, t.vec_out, col0, lane);
         }
-    };
-    if (ep.fast && has_r) load_residual(0);
-#pragma unroll 1
-    for (int c = 0; c < nch; ++c) {
-        uint32_t r[32];
-        __syncwarp();
-        tmem_ld<32>(t_row + c * 32, r);
-        tmem_ld_wait();
-        process(r, c);
+    }
+}
+
+template <int BN, bool OUT8>
+__device__ __forceinline__ void act_tile(const ActTile& t, ActResidual& res, float& m_out, int phase, int lane) {
+    if (t.row0 >= t.m_end) return;  // no row of this warp exists
+    switch (t.act) {
+        case FP8_ACT_NONE: act_blocks<BN, FP8_ACT_NONE, OUT8>(t, res, m_out, phase, lane); break;
+        case FP8_ACT_RELU: act_blocks<BN, FP8_ACT_RELU, OUT8>(t, res, m_out, phase, lane); break;
+        case FP8_ACT_GELU: act_blocks<BN, FP8_ACT_GELU, OUT8>(t, res, m_out, phase, lane); break;
+        case FP8_ACT_GELU_TANH: act_blocks<BN, FP8_ACT_GELU_TANH, OUT8>(t, res, m_out, phase, lane); break;
+        default: act_blocks<BN, FP8_ACT_SILU, OUT8>(t, res, m_out, phase, lane); break;
     }
 }
 
@@ -517,11 +621,12 @@ __device__ __forceinline__ void epilogue_act(const GemmParams& p, const EpArgs<t
 // B_MN only give the defaults and BN is the widest tile.
 template <int BN, bool A_MN, bool B_MN, int STAGES, bool HAS_BIAS, int CTAS, bool SPLIT, bool SWAP, bool OUT8,
           bool GROUP = false, bool EP = false>
-__global__ void __maxnreg__(168)
+__global__ void __maxnreg__(EP && !SWAP ? kActRegs : 168)
 fp8_gemm_kernel(const __grid_constant__ CUtensorMap tm_a, const __grid_constant__ CUtensorMap tm_b,
                 const __grid_constant__ CUtensorMap tm_c, const GemmParams p,
                 const __grid_constant__ GroupTab<GROUP> grp, const __grid_constant__ EpArgs<EP> ep) {
     using L = Smem<BN, STAGES, CTAS, EP ? 4 : 3>;
+    constexpr int ET = epi_threads(EP, SWAP);
     static_assert(!EP || (HAS_BIAS && !GROUP), "an activation epilogue always has its bias slots");
     static_assert(!(B_MN && CTAS == 2 && BN != 256), "MN-major B halves must be whole 128-byte atoms");
     static_assert(!GROUP || (CTAS == 1 && !SPLIT && !SWAP && !OUT8), "grouped launches use plain one-SM tiles");
@@ -565,7 +670,7 @@ fp8_gemm_kernel(const __grid_constant__ CUtensorMap tm_a, const __grid_constant_
         }
         for (int b = 0; b < 2; ++b) {
             mbar_init(bar_tfull + 8 * b, 1);
-            mbar_init(bar_tempty + 8 * b, CTAS * kEpiThreads);
+            mbar_init(bar_tempty + 8 * b, CTAS * ET);
         }
         if (csplit) mbar_init(bar_red, uint32_t(split - 1) * kEpiThreads);
         fence_mbar_init();
@@ -764,7 +869,7 @@ fp8_gemm_kernel(const __grid_constant__ CUtensorMap tm_a, const __grid_constant_
         griddep_launch();
         const int q = warp & 3;             // TMEM lane quarter this warp may access
         const int row_in_tile = q * 32 + lane;
-        const int etid = threadIdx.x - 64;  // 0 .. kEpiThreads-1
+        const int etid = threadIdx.x - 64;  // 0 .. ET-1
         const bool store_lead = etid == 0;  // issues the TMA stores
         const uint32_t stg0 = s_base + L::kStgOffset;
         int n_st = 0;  // TMA stores issued so far (they take the staging tiles in turn)
@@ -810,31 +915,66 @@ fp8_gemm_kernel(const __grid_constant__ CUtensorMap tm_a, const __grid_constant_
             const int buf = it & 1;
             const uint32_t acc_phase = (it >> 1) & 1;
             const int m0 = mb * BM * CTAS + int(rank) * BM;  // this CTA's first output row
-            if (HAS_BIAS && !SWAP) {
+            auto bias_at = [&](int col) {
+                float v = 0.0f;
+                if (col < N && bias_kind != 0) {  // a grouped launch may mix problems with and without bias
+                    if (bias_kind == 1) {
+                        v = __uint_as_float(uint32_t(__ldg(static_cast<const uint16_t*>(bias_ptr) + col)) << 16);
+                    } else {
+                        v = __fdiv_rn(fp8_to_f32(__ldg(static_cast<const uint8_t*>(bias_ptr) + col), bias_fmt),
+                                      bscale);
+                    }
+                }
+                return v;
+            };
+            if (HAS_BIAS && !SWAP && !EP) {
                 // the tile's BN bias values, dequantized once into shared memory
                 epilogue_bar();  // the previous tile's readers are done
-                for (int j = etid; j < ebn; j += kEpiThreads) {
-                    const int col = n_base + nb * ebn + j;
-                    float v = 0.0f;
-                    if (col < N && bias_kind != 0) {  // a grouped launch may mix problems with and without bias
-                        if (bias_kind == 1) {
-                            v = __uint_as_float(uint32_t(__ldg(static_cast<const uint16_t*>(bias_ptr) + col)) << 16);
-                        } else {
-                            v = __fdiv_rn(fp8_to_f32(__ldg(static_cast<const uint8_t*>(bias_ptr) + col), bias_fmt),
-                                          bscale);
-                        }
-                    }
-                    s_bias[j] = v;
-                }
+                for (int j = etid; j < ebn; j += kEpiThreads) s_bias[j] = bias_at(n_base + nb * ebn + j);
                 epilogue_bar();
+            }
+            // an activation epilogue fetches its bias (a column a thread) and its
+            // first residual block while the accumulator is still being made
+            const int phase = (warp - 2) >> 2;
+            float bias_v = 0.0f;
+            ActTile at;
+            ActResidual res;
+            if constexpr (EP && !SWAP) {
+                static_assert(ET >= BN, "a bias column a thread");
+                if (etid < BN) bias_v = bias_at(nb * BN + etid);
+                at.map_out = &tm_c;
+                at.map_z = &ep.tz;
+                at.out = OUT8 ? static_cast<void*>(reinterpret_cast<uint8_t*>(p.out) + int64_t(b) * p.stride_c)
+                              : static_cast<void*>(p.out + int64_t(b) * p.stride_c);
+                at.preact = ep.preact ? ep.preact + int64_t(b) * p.stride_c : nullptr;
+                at.residual = ep.residual ? ep.residual + int64_t(b) * ep.stride_r : nullptr;
+                at.s_bias = s_bias;
+                at.stg = stg0 + uint32_t(warp - 2) * 2048u;
+                at.inv = inv;
+                at.s_out = s_out;
+                at.act = ep.act;
+                at.out_fmt = p.out_fmt;
+                at.row0 = m0 + q * 32;
+                at.m_end = M;
+                at.col_first = nb * BN;
+                at.N = N;
+                at.b = b;
+                at.tma_out = at.vec_out = tma_store;
+                at.tma_z = at.vec_z = ep.fast;
+                at.has = true;
+                if (!OUT8 && at.residual && ep.fast) res.load(at, phase, lane);
             }
             // every lane waits, then all epilogue warps agree (and each warp
             // reconverges) before the warp-collective TMEM loads. After a wait
             // gave up, they all keep walking the units without waiting, so that
             // they still meet at every named barrier.
             if (!failed) failed = !wait_bounded(bar_tfull + 8 * buf, acc_phase);
-            failed = epilogue_bar_or(failed);
+            failed = epilogue_bar_or<ET>(failed);  // the previous tile's readers are done, too
             if (failed) continue;
+            if constexpr (EP && !SWAP) {
+                if (etid < BN) s_bias[etid] = bias_v;
+                epilogue_bar<ET>();
+            }
             tc_fence_after();
             const uint32_t t_row = tmem_base + (uint32_t(q * 32) << 16) + buf * BN;
             // Split K: the unit that arrives last at its tile finishes it; the
@@ -920,8 +1060,8 @@ fp8_gemm_kernel(const __grid_constant__ CUtensorMap tm_a, const __grid_constant_
             uint16_t* orow = SWAP ? out_base + int64_t(b) * p.stride_c + row
                                   : out_base + int64_t(b) * p.stride_c + int64_t(row) * N;
             if constexpr (EP && !SWAP) {
-                epilogue_act<BN, OUT8, L>(p, ep, &tm_c, t_row, s_bias, stg0, n_st, q, lane, store_lead, inv, s_out, m_out,
-                                          m0, nb * BN, b, M, N, vec_store);
+                at.t_row = t_row;
+                act_tile<BN, OUT8>(at, res, m_out, phase, lane);
             }
             if constexpr (!EP && !SPLIT && !SWAP && !OUT8) {
                 if (tma_store) {
@@ -1139,17 +1279,18 @@ fp8_gemm_kernel(const __grid_constant__ CUtensorMap tm_a, const __grid_constant_
         // the staging tiles must outlive the stores that read them; the global
         // writes themselves complete with the grid (a dependent kernel's
         // griddepcontrol.wait and stream order both see them)
-        if ((GROUP || EP || tma_store) && store_lead) bulk_wait_read<0>();
+        if ((GROUP || EP || tma_store) && (EP && !SWAP ? lane == 0 : store_lead)) bulk_wait_read<0>();
         if constexpr (OUT8) {
             // the CTA's amax of the output: one atomicMax, then a ticket; the
             // CTA holding the last ticket folds it into the output's ring
             uint32_t bits = __reduce_max_sync(0xffffffffu, __float_as_uint(m_out));
-            epilogue_bar();  // the bias slots are free now
+            epilogue_bar<ET>();  // the bias slots are free now
             uint32_t* red = reinterpret_cast<uint32_t*>(s_bias);
-            if (lane == 0) red[q] = bits;
-            epilogue_bar();
+            if (lane == 0) red[warp - 2] = bits;
+            epilogue_bar<ET>();
             if (etid == 0) {
                 bits = max(max(red[0], red[1]), max(red[2], red[3]));
+                for (int w = 4; w < ET / 32; ++w) bits = max(bits, red[w]);
                 fp8_ring* ring = p.out_ring;
                 if (bits != 0u) atomicMax(&ring->amax_bits, bits);
                 const uint32_t ticket = atom_add_acq_rel(&ring->ticket, 1u);
@@ -1224,8 +1365,10 @@ bool make_map(CUtensorMap* map, const void* base, uint64_t inner, uint64_t outer
 }
 
 // 3-D map over the bf16 output (N, M, batch), 32-column x 128-row boxes with
-// a 64-byte swizzle matching the epilogue's staging tiles.
-bool make_out_map(CUtensorMap* map, void* base, uint64_t n, uint64_t m, uint64_t batch, uint64_t batch_stride_bytes) {
+// a 64-byte swizzle matching the epilogue's staging tiles (32 rows for a warp
+// of an activation epilogue).
+bool make_out_map(CUtensorMap* map, void* base, uint64_t n, uint64_t m, uint64_t batch, uint64_t batch_stride_bytes,
+                  uint32_t box_rows = BM) {
     EncodeTiledFn fn = encode_fn();
     if (!fn) return false;
     if (batch <= 1 || batch_stride_bytes == 0) {
@@ -1234,10 +1377,28 @@ bool make_out_map(CUtensorMap* map, void* base, uint64_t n, uint64_t m, uint64_t
     }
     cuuint64_t dims[3] = {n, m, batch};
     cuuint64_t strides[2] = {n * 2, batch_stride_bytes};
-    cuuint32_t box[3] = {32, uint32_t(BM), 1};
+    cuuint32_t box[3] = {32, box_rows, 1};
     cuuint32_t estr[3] = {1, 1, 1};
     return fn(map, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 3, base, dims, strides, box, estr, CU_TENSOR_MAP_INTERLEAVE_NONE,
               CU_TENSOR_MAP_SWIZZLE_64B, CU_TENSOR_MAP_L2_PROMOTION_NONE, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) ==
+           CUDA_SUCCESS;
+}
+
+// 3-D map over FP8 output codes (N, M, batch), 32-column x 32-row boxes with
+// a 32-byte swizzle.
+bool make_out8_map(CUtensorMap* map, void* base, uint64_t n, uint64_t m, uint64_t batch, uint64_t batch_stride) {
+    EncodeTiledFn fn = encode_fn();
+    if (!fn) return false;
+    if (batch <= 1 || batch_stride == 0) {
+        batch = 1;
+        batch_stride = (n * m + 15) / 16 * 16;
+    }
+    cuuint64_t dims[3] = {n, m, batch};
+    cuuint64_t strides[2] = {n, batch_stride};
+    cuuint32_t box[3] = {32, 32, 1};
+    cuuint32_t estr[3] = {1, 1, 1};
+    return fn(map, CU_TENSOR_MAP_DATA_TYPE_UINT8, 3, base, dims, strides, box, estr, CU_TENSOR_MAP_INTERLEAVE_NONE,
+              CU_TENSOR_MAP_SWIZZLE_32B, CU_TENSOR_MAP_L2_PROMOTION_NONE, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) ==
            CUDA_SUCCESS;
 }
 
@@ -1287,14 +1448,18 @@ fp8_status launch_one(const CUtensorMap& ta, const CUtensorMap& tb, const CUtens
     // a cluster split runs each tile's splits as one cluster (every unit in
     // the grid's one round, so the grid is a whole number of clusters)
     const int cluster = p.csplit ? p.split : CTAS;
-    return launch_pdl(kern, units * CTAS, kThreads, L::kAlloc, st, cluster, ta, tb, tc, p, GroupTab<false>{}, ep);
+    return launch_pdl(kern, units * CTAS, 64 + epi_threads(EP, SWAP), L::kAlloc, st, cluster, ta, tb, tc, p,
+                      GroupTab<false>{}, ep);
 }
 
 template <int BN, bool A_MN, bool B_MN, int STAGES, int CTAS, bool SWAP = false, bool OUT8 = false, bool EP = false>
 fp8_status launch(const CUtensorMap& ta, const CUtensorMap& tb, GemmParams p, const HostArgs& h, cudaStream_t st,
                   const EpArgs<EP>& ep = {}) {
     CUtensorMap tc = {};
-    if (p.tma_store && !make_out_map(&tc, p.out, p.N, p.M, h.batch, uint64_t(p.stride_c) * 2)) return FP8_ERR_CUDA;
+    if (p.tma_store && !(EP && OUT8 ? make_out8_map(&tc, p.out, p.N, p.M, h.batch, uint64_t(p.stride_c))
+                                    : make_out_map(&tc, p.out, p.N, p.M, h.batch, uint64_t(p.stride_c) * 2,
+                                                   EP ? 32 : BM)))
+        return FP8_ERR_CUDA;
     if constexpr (EP) {  // always with bias slots; only a swapped problem splits (as a cluster)
         if constexpr (SWAP) {
             if (p.split > 1)
