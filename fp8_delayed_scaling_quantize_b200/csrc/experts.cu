@@ -79,8 +79,8 @@ struct Experts {
     int before;  // maximum of the offsets before this lane's
     int tiles;   // tiles up to and with this lane's experts
     int mine;    // this lane's
-    // the expert found last: its tiles [t0, t1) and rows [lo, hi)
-    int e, t0, t1, lo, hi;
+    // the expert found last: its tiles [t0, t1), units [u0, u1) and rows [lo, hi)
+    int e, t0, t1, u0, u1, lo, hi;
 
     __device__ __forceinline__ int at(int i) const { return min(max(__ldg(offsets + min(i, experts)), 0), rows); }
     __device__ __forceinline__ static int count(int lo, int hi) { return (hi - lo + TILE - 1) / TILE; }
@@ -92,7 +92,7 @@ struct Experts {
         per = (experts + 31) / 32;
         lane = threadIdx.x & 31;
         e = -1;
-        t0 = t1 = 0;
+        t0 = t1 = u0 = u1 = 0;
         const int first = lane * per;
         int m = 0;
         for (int i = 0; i < per; ++i) m = max(m, at(first + i));
@@ -132,9 +132,10 @@ struct Experts {
         if (lane >= per) next = v;
     }
 
-    // The expert that tile t (< total) belongs to.
-    __device__ __forceinline__ void find_tile(int t) {
-        if (t >= t0 && t < t1) return;
+    // The expert that unit u belongs to, `per_tile` units to a tile.
+    __device__ __forceinline__ void find_unit(int u, int per_tile) {
+        if (u >= u0 && u < u1) return;
+        const int t = u / per_tile;
         const int l = __ffs(__ballot_sync(0xffffffffu, tiles > t)) - 1;
         const int base = __shfl_sync(0xffffffffu, tiles - mine, l);
         int v, next;
@@ -152,43 +153,61 @@ struct Experts {
         hi = __shfl_sync(0xffffffffu, next, k);
         t1 = base + __shfl_sync(0xffffffffu, sum, k);
         t0 = t1 - __shfl_sync(0xffffffffu, n, k);
+        u0 = t0 * per_tile;
+        u1 = t1 * per_tile;
     }
 
-    // Expert x (< experts).
-    __device__ __forceinline__ void find_expert(int x) {
-        if (x == e) return;
+    // The same where every expert has `per_expert` units.
+    __device__ __forceinline__ void find_expert(int u, int per_expert) {
+        if (u >= u0 && u < u1) return;
+        const int x = u / per_expert;
         int v, next;
         group(x / per, v, next);
         e = x;
+        u0 = x * per_expert;
+        u1 = u0 + per_expert;
         lo = __shfl_sync(0xffffffffu, v, x % per);
         hi = __shfl_sync(0xffffffffu, next, x % per);
     }
 };
 
+// Tile i of one expert's mt x nt tiles: groups of 16 tile rows, M-fastest
+// inside (tile_coords, for tiles that mostly fit one group).
+__device__ __forceinline__ void expert_tile(int i, int mt, int nt, int& mb, int& nb) {
+    constexpr int kGroup = 16;
+    int first = 0;
+    if (i >= kGroup * nt) {
+        const int g = i / (kGroup * nt);
+        first = g * kGroup;
+        i -= first * nt;
+    }
+    const int rows = min(kGroup, mt - first);
+    nb = i / rows;
+    mb = first + i - nb * rows;
+}
+
 // Work unit u.
 template <int BN, int KIND, bool SWAP, int TILE>
 __device__ __forceinline__ Item item_of(Experts<TILE>& x, const ExpertParams& p, int u) {
     Item it;
-    int mb, nb, b;
+    int mb, nb;
     if constexpr (KIND == kSumTN) {
-        const int per = p.m_tiles * p.n_tiles, e = u / per;
-        tile_coords(u - e * per, TileWalk{p.m_tiles, p.n_tiles, 16}, mb, nb, b);
-        x.find_expert(e);
-        it.m0 = mb * BM;
+        x.find_expert(u, p.m_tiles * p.n_tiles);
+        expert_tile(u - x.u0, p.m_tiles, p.n_tiles, mb, nb);
+        it.m0 = mb * TILE;
         it.m_end = p.M;
         it.n0 = nb * BN;
         it.k_row = x.lo;
         it.k_end = x.hi;
         it.kbs = (x.hi - x.lo + BK - 1) / BK;
     } else {
-        x.find_tile(u / p.n_tiles);
-        const int t = u - x.t0 * p.n_tiles, mt = x.t1 - x.t0;
+        x.find_unit(u, p.n_tiles);
         if constexpr (SWAP) {
-            mb = t % mt;  // the row tiles of one weight tile one after the other
-            nb = t / mt;
+            nb = (u - x.u0) / (x.t1 - x.t0);  // the row tiles of one weight tile one after the other
+            mb = u - x.u0 - nb * (x.t1 - x.t0);
             it.n0 = nb * BM;
         } else {
-            tile_coords(t, TileWalk{mt, p.n_tiles, 16}, mb, nb, b);
+            expert_tile(u - x.u0, x.t1 - x.t0, p.n_tiles, mb, nb);
             it.n0 = nb * BN;
         }
         it.m0 = x.lo + mb * TILE;
@@ -201,19 +220,25 @@ __device__ __forceinline__ Item item_of(Experts<TILE>& x, const ExpertParams& p,
 }
 
 // KIND, SWAP: see the head of the file. BN: output columns of a tile, or
-// token rows of a swapped one.
-template <int BN, int KIND, int STAGES, bool SWAP>
+// token rows of a swapped one. CTAS = 2: a pair of CTAs on 256 x BN tiles
+// (cta_group::2): each loads its 128 rows of A and half of B and writes its
+// own 128 rows of the output, so an SM takes in a third less per MMA.
+template <int BN, int KIND, int STAGES, bool SWAP, int CTAS>
 __global__ void __maxnreg__(SWAP ? 168 : kActRegs)
 expert_kernel(const __grid_constant__ CUtensorMap tm_a, const __grid_constant__ CUtensorMap tm_b,
               const __grid_constant__ CUtensorMap tm_c, const __grid_constant__ CUtensorMap tm_z, const ExpertParams p) {
-    using L = Smem<BN, STAGES, 1, SWAP ? 3 : 4>;
+    using L = Smem<BN, STAGES, CTAS, SWAP ? 3 : 4>;
+    static_assert(CTAS == 1 || (BN == 256 && !SWAP), "a pair's half of an MN-major B is one 128-byte atom");
     constexpr int ET = epi_threads(true, SWAP);
-    constexpr int TILE = SWAP ? BN : BM;
+    constexpr int TILE = SWAP ? BN : BM * CTAS;
     // majors of the MMA's operands: K-major unless the stored rows run along K
     constexpr bool A_MN = SWAP ? KIND == kRowsNN : KIND == kSumTN;
     constexpr bool B_MN = !SWAP && KIND != kRowsNT;
     extern __shared__ __align__(1024) uint8_t smem_raw[];
     uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
+    if constexpr (L::kAct) {
+        if (!smem_fits<L>(smem_raw, smem)) return;
+    }
     const uint32_t s_a = smem_addr(smem);
     const uint32_t s_b = s_a + STAGES * L::kABytes;
     const uint32_t bar_full = s_a + L::kBarOffset;
@@ -223,6 +248,9 @@ expert_kernel(const __grid_constant__ CUtensorMap tm_a, const __grid_constant__ 
     uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(smem + L::kBarOffset + (2 * STAGES + 4) * 8);
     float* s_bias = reinterpret_cast<float*>(smem + L::kBiasOffset);
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    const uint32_t rank = CTAS == 2 ? cluster_ctarank() : 0u;  // 0 = the pair's leader
+    const bool leader = rank == 0;
+    const int unit0 = blockIdx.x / CTAS, unit_step = gridDim.x / CTAS;
 
     if (warp == 0 && lane == 0) {
         for (int s = 0; s < STAGES; ++s) {
@@ -231,7 +259,7 @@ expert_kernel(const __grid_constant__ CUtensorMap tm_a, const __grid_constant__ 
         }
         for (int b = 0; b < 2; ++b) {
             mbar_init(bar_tfull + 8 * b, 1);
-            mbar_init(bar_tempty + 8 * b, ET);
+            mbar_init(bar_tempty + 8 * b, CTAS * ET);
         }
         fence_mbar_init();
         tma_prefetch(&tm_a);
@@ -242,11 +270,12 @@ expert_kernel(const __grid_constant__ CUtensorMap tm_a, const __grid_constant__ 
         }
     }
     if (warp == 1) {
-        tmem_alloc<1>(smem_addr(tmem_slot), L::kTmemCols);
-        tmem_relinquish<1>();
+        tmem_alloc<CTAS>(smem_addr(tmem_slot), L::kTmemCols);
+        tmem_relinquish<CTAS>();
     }
     tc_fence_before();
     __syncthreads();
+    if (CTAS == 2) cluster_sync();  // the pair's barriers exist before any remote arrive
     tc_fence_after();
     const uint32_t tmem_base = *tmem_slot;
     griddep_wait();
@@ -261,33 +290,39 @@ expert_kernel(const __grid_constant__ CUtensorMap tm_a, const __grid_constant__ 
         int stage = 0;
         uint32_t phase = 0;
         bool ok = true;
-        for (int u = blockIdx.x; u < units && ok; u += gridDim.x) {
+        for (int u = unit0; u < units && ok; u += unit_step) {
             const Item it = item_of<BN, KIND, SWAP>(x, p, u);
             for (int kb = 0; kb < it.kbs; ++kb) {
                 if (!wait_bounded_warp(bar_empty + 8 * stage, phase ^ 1)) { ok = false; break; }
                 const uint32_t full = bar_full + 8 * stage;
                 const uint32_t da = s_a + stage * L::kABytes, db = s_b + stage * L::kBBytes;
                 if (issuer) {
-                    mbar_arrive_expect_tx(full, uint32_t(L::kStageBytes));
+                    if (leader) mbar_arrive_expect_tx(full, uint32_t(L::kStageTx));
+                    // a pair's loads complete on the leader's barrier
+                    const uint32_t bar = CTAS == 2 ? map_to_rank(full, 0) : full;
+                    auto load = [&](uint32_t dst, const CUtensorMap* map, int c0, int c1, int c2) {
+                        if (CTAS == 2) tma_load_3d_pair(dst, map, bar, c0, c1, c2);
+                        else           tma_load_3d(dst, map, bar, c0, c1, c2);
+                    };
+                    constexpr int kAtoms = BN / CTAS / 128;  // 128-column atoms of an MN-major B
+                    const int m0 = it.m0 + int(rank) * BM, n0 = it.n0 + int(rank) * (BN / CTAS);
                     if constexpr (KIND == kSumTN) {
                         const int first = it.k_row + kb * BK;
                         const int r0 = min(it.k_end - first, BK) - BK;  // 0, or negative in the last block
-                        tma_load_3d(da, &tm_a, full, it.m0, r0, first);
+                        load(da, &tm_a, m0, r0, first);
 #pragma unroll
-                        for (int h = 0; h < BN / 128; ++h)
-                            tma_load_3d(db + h * 128 * BK, &tm_b, full, it.n0 + h * 128, r0, first);
+                        for (int h = 0; h < kAtoms; ++h) load(db + h * 128 * BK, &tm_b, n0 + h * 128, r0, first);
                     } else if constexpr (SWAP) {
-                        if (A_MN) tma_load_3d(da, &tm_b, full, it.n0, kb * BK, it.e);
-                        else      tma_load_3d(da, &tm_b, full, kb * BK, it.n0, it.e);
-                        tma_load_3d(db, &tm_a, full, kb * BK, it.m0, 0);
+                        if (A_MN) load(da, &tm_b, it.n0, kb * BK, it.e);
+                        else      load(da, &tm_b, kb * BK, it.n0, it.e);
+                        load(db, &tm_a, kb * BK, it.m0, 0);
                     } else {
-                        tma_load_3d(da, &tm_a, full, kb * BK, it.m0, 0);
+                        load(da, &tm_a, kb * BK, m0, 0);
                         if (B_MN) {
 #pragma unroll
-                            for (int h = 0; h < BN / 128; ++h)
-                                tma_load_3d(db + h * 128 * BK, &tm_b, full, it.n0 + h * 128, kb * BK, it.e);
+                            for (int h = 0; h < kAtoms; ++h) load(db + h * 128 * BK, &tm_b, n0 + h * 128, kb * BK, it.e);
                         } else {
-                            tma_load_3d(db, &tm_b, full, kb * BK, it.n0, it.e);
+                            load(db, &tm_b, kb * BK, n0, it.e);
                         }
                     }
                 }
@@ -307,8 +342,8 @@ expert_kernel(const __grid_constant__ CUtensorMap tm_a, const __grid_constant__ 
         const uint64_t b_desc0 = B_MN ? smem_desc_sw128(s_b, 128 * BK, 1024) : smem_desc_sw128(s_b, 16, 1024);
         int stage = 0, done = 0;
         uint32_t phase = 0;
-        bool ok = true;
-        for (int u = blockIdx.x; u < units && ok; u += gridDim.x) {
+        bool ok = leader;  // a pair's MMAs are its leader's
+        for (int u = unit0; u < units && ok; u += unit_step) {
             const Item it = item_of<BN, KIND, SWAP>(x, p, u);
             if (it.kbs == 0) continue;  // an expert without rows: the epilogue writes its zeros
             const int buf = done & 1;
@@ -317,15 +352,19 @@ expert_kernel(const __grid_constant__ CUtensorMap tm_a, const __grid_constant__ 
             for (int kb = 0; kb < it.kbs; ++kb) {
                 if (!wait_bounded_warp(bar_full + 8 * stage, phase)) { ok = false; break; }
                 if (issuer) {
-                    mma_kblock_f8f6f4<1>(tmem_base + buf * BN, a_desc0 + uint64_t(stage) * (L::kABytes >> 4),
+                    mma_kblock_f8f6f4<CTAS>(tmem_base + buf * BN, a_desc0 + uint64_t(stage) * (L::kABytes >> 4),
                                          b_desc0 + uint64_t(stage) * (L::kBBytes >> 4), A_MN ? 256u : 2u,
                                          B_MN ? 256u : 2u, p.idesc, kb != 0);
-                    mma_commit(bar_empty + 8 * stage);
+                    if (CTAS == 2) mma_commit_pair(bar_empty + 8 * stage);
+                    else           mma_commit(bar_empty + 8 * stage);
                 }
                 __syncwarp();
                 if (++stage == STAGES) { stage = 0; phase ^= 1; }
             }
-            if (issuer) mma_commit(bar_tfull + 8 * buf);
+            if (issuer) {
+                if (CTAS == 2) mma_commit_pair(bar_tfull + 8 * buf);
+                else           mma_commit(bar_tfull + 8 * buf);
+            }
             __syncwarp();
             ++done;
         }
@@ -333,7 +372,6 @@ expert_kernel(const __grid_constant__ CUtensorMap tm_a, const __grid_constant__ 
         // ----------------------------------------------------- epilogue ---
         const int q = warp & 3;  // TMEM lane quarter this warp may access
         const int row_in_tile = q * 32 + lane;
-        const int etid = threadIdx.x - 64;
         const int phase = (warp - 2) >> 2;
         const uint32_t stg0 = s_a + L::kStgOffset;
         const float inv_a = 1.0f / __ldg(p.sa);
@@ -341,31 +379,34 @@ expert_kernel(const __grid_constant__ CUtensorMap tm_a, const __grid_constant__ 
         float unused = 0.0f;
         ActResidual none;
         bool failed = false;
-        if constexpr (KIND == kSumTN) {  // no bias
-            for (int j = etid; j < BN; j += ET) s_bias[j] = 0.0f;
-            epilogue_bar<ET>();
-        }
-        for (int u = blockIdx.x; u < units; u += gridDim.x) {
-            const Item it = item_of<BN, KIND, SWAP>(x, p, u);
-            const float inv = inv_a * (1.0f / __ldg(p.sb + int64_t(it.e) * p.sb_stride));
+        if constexpr (!SWAP) s_bias[(warp - 2) * 32 + lane] = 0.0f;
+        // what a unit needs from global memory is asked for one unit early
+        Item next = {};
+        float scale_next = 1.0f;
+        constexpr int kBlocks = SWAP ? 1 : kActBlocks<BN>;
+        float bias[kBlocks] = {}, bias_next[kBlocks] = {};  // this lane's column of each block (swapped: its column)
+        auto ask = [&](int u) {
+            next = item_of<BN, KIND, SWAP>(x, p, u);
+            scale_next = __ldg(p.sb + int64_t(next.e) * p.sb_stride);
+            if (!p.bias) return;
+#pragma unroll
+            for (int i = 0; i < kBlocks; ++i) {
+                const int col = next.n0 + (SWAP ? row_in_tile : (phase + i * kActPhases) * 32 + lane);
+                bias_next[i] = col < p.N ? bf16_value(__ldg(p.bias + int64_t(next.e) * p.N + col)) : 0.0f;
+            }
+        };
+        if (unit0 < units) ask(unit0);
+        for (int u = unit0; u < units; u += unit_step) {
+            const Item it = next;
+            const float inv = inv_a * (1.0f / scale_next);
+#pragma unroll
+            for (int i = 0; i < kBlocks; ++i) bias[i] = bias_next[i];
+            if (u + unit_step < units) ask(u + unit_step);
             const bool has = it.kbs > 0;
             const int buf = done & 1;
-            float bias_v = 0.0f;  // of column etid
-            if constexpr (!SWAP && KIND != kSumTN) {
-                const int col = it.n0 + etid;
-                if (p.bias && etid < BN && col < p.N) bias_v = bf16_value(__ldg(p.bias + int64_t(it.e) * p.N + col));
-            }
-            float bias_row = 0.0f;
-            if (SWAP && p.bias && it.n0 + row_in_tile < p.N)
-                bias_row = bf16_value(__ldg(p.bias + int64_t(it.e) * p.N + it.n0 + row_in_tile));
             if (has) {
-                if (!failed) failed = !wait_bounded(bar_tfull + 8 * buf, (done >> 1) & 1);
-                failed = epilogue_bar_or<ET>(failed);  // the previous tile's readers are done, too
-                if (failed) continue;
-                if constexpr (!SWAP && KIND != kSumTN) {
-                    if (etid < BN) s_bias[etid] = bias_v;
-                    epilogue_bar<ET>();
-                }
+                if (!failed) failed = !wait_bounded_warp(bar_tfull + 8 * buf, (done >> 1) & 1);
+                if (failed) continue;  // the other warps find it out for themselves
                 tc_fence_after();
             }
             const uint32_t t_row = tmem_base + (uint32_t(q * 32) << 16) + buf * BN;
@@ -381,7 +422,7 @@ expert_kernel(const __grid_constant__ CUtensorMap tm_a, const __grid_constant__ 
                     tmem_ld_wait();
                     float y[16];
 #pragma unroll
-                    for (int i = 0; i < 16; ++i) y[i] = fmaf(__uint_as_float(r[i]), inv, bias_row);
+                    for (int i = 0; i < 16; ++i) y[i] = fmaf(__uint_as_float(r[i]), inv, bias[0]);
                     if (col < p.N) {
                         const int64_t at = int64_t(r0) * p.N + col;
                         if (p.preact) {
@@ -402,14 +443,15 @@ expert_kernel(const __grid_constant__ CUtensorMap tm_a, const __grid_constant__ 
                 t.out = KIND == kSumTN ? p.out + int64_t(it.e) * p.M * p.N : p.out;
                 t.preact = p.preact;
                 t.residual = nullptr;
-                t.s_bias = s_bias;
+                t.s_bias = s_bias + (warp - 2) * 32;
+                t.has_bias = KIND != kSumTN && p.bias != nullptr;
                 t.t_row = t_row;
                 t.stg = stg0 + uint32_t(warp - 2) * 2048u;
                 t.inv = inv;
                 t.s_out = 1.0f;
                 t.act = p.act;
                 t.out_fmt = 0;
-                t.row0 = it.m0 + q * 32;
+                t.row0 = it.m0 + int(rank) * BM + q * 32;
                 t.m_end = it.m_end;
                 t.col_first = it.n0;
                 t.N = p.N;
@@ -419,14 +461,15 @@ expert_kernel(const __grid_constant__ CUtensorMap tm_a, const __grid_constant__ 
                 t.vec_out = t.vec_z = p.fast;
                 t.has = has;
                 if constexpr (KIND == kSumTN) {
-                    if (t.row0 < t.m_end) act_blocks<BN, FP8_ACT_NONE, false>(t, none, unused, phase, lane);
+                    if (t.row0 < t.m_end) act_blocks<BN, FP8_ACT_NONE, false>(t, none, bias, unused, phase, lane);
                 } else {
-                    act_tile<BN, false>(t, none, unused, phase, lane);
+                    act_tile<BN, false>(t, none, bias, unused, phase, lane);
                 }
             }
             if (has) {
                 tc_fence_before();
-                mbar_arrive(bar_tempty + 8 * buf);
+                if (CTAS == 2) mbar_arrive_cluster(map_to_rank(bar_tempty + 8 * buf, 0));
+                else           mbar_arrive(bar_tempty + 8 * buf);
                 ++done;
             }
         }
@@ -435,10 +478,11 @@ expert_kernel(const __grid_constant__ CUtensorMap tm_a, const __grid_constant__ 
 
     tc_fence_before();
     __syncthreads();
+    if (CTAS == 2) cluster_sync();  // neither CTA leaves while the other may still signal it
     tc_fence_after();
     if (warp == 1) {
         __syncwarp();
-        tmem_dealloc<1>(tmem_base, L::kTmemCols);
+        tmem_dealloc<CTAS>(tmem_base, L::kTmemCols);
     }
 }
 
@@ -456,11 +500,11 @@ bool make_block_map(CUtensorMap* map, const void* base, uint64_t cols, uint64_t 
               CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 
-template <int BN, int KIND, int STAGES, bool SWAP>
+template <int BN, int KIND, int STAGES, bool SWAP, int CTAS = 1>
 fp8_status launch_experts(const CUtensorMap& ta, const CUtensorMap& tb, const CUtensorMap& tc, const CUtensorMap& tz,
                           ExpertParams p, int fa, int fb, int64_t most_units, cudaStream_t st) {
-    using L = Smem<BN, STAGES, 1, SWAP ? 3 : 4>;
-    auto kern = expert_kernel<BN, KIND, STAGES, SWAP>;
+    using L = Smem<BN, STAGES, CTAS, SWAP ? 3 : 4>;
+    auto kern = expert_kernel<BN, KIND, STAGES, SWAP, CTAS>;
     static bool attr_set[64] = {false};
     int dev = 0;
     if (cudaGetDevice(&dev) != cudaSuccess || dev < 0 || dev >= 64) return FP8_ERR_CUDA;
@@ -470,9 +514,22 @@ fp8_status launch_experts(const CUtensorMap& ta, const CUtensorMap& tb, const CU
         attr_set[dev] = true;
     }
     p.idesc = SWAP ? instr_desc_f8(fb, fa, KIND == kRowsNN, 0, BM, BN)
-                   : instr_desc_f8(fa, fb, KIND == kSumTN, KIND != kRowsNT, BM, BN);
-    const int grid = int(most_units < sm_count() ? most_units : sm_count());
-    return launch_pdl(kern, grid, 64 + epi_threads(true, SWAP), L::kAlloc, st, 1, ta, tb, tc, tz, p);
+                   : instr_desc_f8(fa, fb, KIND == kSumTN, KIND != kRowsNT, BM * CTAS, BN);
+    const int64_t slots = sm_count() / CTAS;
+    const int grid = int(most_units < slots ? most_units : slots) * CTAS;
+    return launch_pdl(kern, grid, 64 + epi_threads(true, SWAP), L::kAlloc, st, CTAS, ta, tb, tc, tz, p);
+}
+
+// Whether an SM pair's 256 x 256 tiles serve the call. They take in less per
+// MMA but pad an expert's last rows to 256 and halve the grid's grain, so they
+// pay with many rows an expert and a long main loop. Measured on B200 (us, one
+// SM against pairs): 8 experts of 2048 rows, 4096 x 2048 121 -> 111, its dX
+// (32 k-blocks) 114 -> 107, its dW (16) 119 -> 110; but with 8 k-blocks 67 ->
+// 71 even for one expert of 16384 rows, and 32 experts of 512 rows 82 -> 92,
+// dX 68.5 -> 70.9, dW (4) 97 -> 114.
+inline bool use_pair(bool sum, int64_t rows, int64_t M, int64_t N, int64_t K, int64_t experts) {
+    const int64_t kb = (sum ? rows / experts : K) / BK;
+    return N > 128 && kb >= 16 && (sum ? M > BM : rows >= 1024 * experts);
 }
 
 }  // namespace
@@ -524,14 +581,16 @@ extern "C" fp8_status fp8_mm_experts(const uint8_t* a8, fp8_fmt fa, const uint8_
         return rows / tile + with_rows;
     };
     constexpr int64_t kMost = int64_t(1) << 31;
+    constexpr int BN = 256;
     if (sum) {
-        constexpr int BN = 256;
-        p.m_tiles = int((M + BM - 1) / BM);
+        const bool pair = use_pair(sum, rows, M, N, K, experts);
+        p.m_tiles = int((M + BM * (pair ? 2 : 1) - 1) / (BM * (pair ? 2 : 1)));
         p.n_tiles = int((N + BN - 1) / BN);
         const int64_t units = int64_t(experts) * p.m_tiles * p.n_tiles;
         if (units >= kMost) return FP8_ERR_UNSUPPORTED;
         if (!make_block_map(&ta, a8, M, rows) || !make_block_map(&tb, b8, N, rows)) return FP8_ERR_CUDA;
         if (p.fast && !make_out_map(&tc, out, N, M, experts, uint64_t(M) * N * 2, 32)) return FP8_ERR_CUDA;
+        if (pair) return launch_experts<BN, kSumTN, 6, false, 2>(ta, tb, tc, tz, p, fa, fb, units, st);
         return launch_experts<BN, kSumTN, 4, false>(ta, tb, tc, tz, p, fa, fb, units, st);
     }
     const bool nn = layout == FP8_NN;
@@ -551,16 +610,19 @@ extern "C" fp8_status fp8_mm_experts(const uint8_t* a8, fp8_fmt fa, const uint8_
         return nn ? launch_experts<32, kRowsNN, 9, true>(ta, tb, tc, tz, p, fa, fb, units, st)
                   : launch_experts<32, kRowsNT, 9, true>(ta, tb, tc, tz, p, fa, fb, units, st);
     }
-    constexpr int BN = 256;
+    const bool pair = use_pair(sum, rows, M, N, K, experts);
     p.n_tiles = int((N + BN - 1) / BN);
-    const int64_t units = most(BM) * p.n_tiles;
+    const int64_t units = most(BM * (pair ? 2 : 1)) * p.n_tiles;
     if (units >= kMost) return FP8_ERR_UNSUPPORTED;
     const bool ok = make_map(&ta, a8, K, rows, 1, 0, BK, BM) &&
                     (nn ? make_map(&tb, b8, N, K, experts, uint64_t(N) * K, 128, BK)
-                        : make_map(&tb, b8, K, N, experts, uint64_t(N) * K, BK, BN));
+                        : make_map(&tb, b8, K, N, experts, uint64_t(N) * K, BK, pair ? BN / 2 : BN));
     if (!ok) return FP8_ERR_CUDA;
     if (p.fast && !make_out_map(&tc, out, N, rows, 1, 0, 32)) return FP8_ERR_CUDA;
     if (p.fast && preact && !make_out_map(&tz, preact, N, rows, 1, 0, 32)) return FP8_ERR_CUDA;
+    if (pair)
+        return nn ? launch_experts<BN, kRowsNN, 6, false, 2>(ta, tb, tc, tz, p, fa, fb, units, st)
+                  : launch_experts<BN, kRowsNT, 6, false, 2>(ta, tb, tc, tz, p, fa, fb, units, st);
     return nn ? launch_experts<BN, kRowsNN, 4, false>(ta, tb, tc, tz, p, fa, fb, units, st)
               : launch_experts<BN, kRowsNT, 4, false>(ta, tb, tc, tz, p, fa, fb, units, st);
 }

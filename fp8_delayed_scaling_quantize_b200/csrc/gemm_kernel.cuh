@@ -292,14 +292,26 @@ struct Smem {
     static constexpr int kStgBytes = BM * 32 * 2;
     static constexpr int kStgOffset = STAGES * kStageBytes;  // a multiple of 1024
     static constexpr int kBiasOffset = kStgOffset + kStgBufs * kStgBytes;  // BN fp32 bias values
-    static constexpr int kBarOffset = kBiasOffset + BN * 4;
+    static constexpr bool kAct = STG == 4;  // an activation epilogue: 32 bias values for each of its warps
+    static constexpr int kBarOffset = kBiasOffset + (kAct ? 2048 : BN * 4);
     // full[S], empty[S], tmem_full[2], tmem_empty[2], then the TMEM slot and the split ticket
     static constexpr int kBytes = kBarOffset + (2 * STAGES + 4) * 8 + 16;
-    static constexpr int kAlloc = kBytes + 1024;  // room to align the base to 1024
+    // room to align the base to 1024. The base is declared so; an activation
+    // epilogue has no full KB left for one that is not, and gives up then
+    static constexpr int kAlloc = kAct ? 227 * 1024 : kBytes + 1024;
     static constexpr uint32_t kTmemCols = 2 * BN < 32 ? 32 : 2 * BN;
     static_assert(kStgOffset % 1024 == 0, "staging tiles need 1024-byte alignment");
-    static_assert(kAlloc <= 227 * 1024, "shared memory per CTA");
+    static_assert(kAlloc <= 227 * 1024 && kBytes <= kAlloc, "shared memory per CTA");
 };
+
+// Whether a CTA's plan fits its shared memory from the aligned base on (for
+// every thread of the grid alike). If not, the device error word is set.
+template <typename L>
+__device__ __forceinline__ bool smem_fits(const uint8_t* raw, const uint8_t* base) {
+    if (base - raw + L::kBytes <= L::kAlloc) return true;
+    atomicOr(&g_device_error, 1u);
+    return false;
+}
 
 // The tile walk's scalars, read once into registers.
 struct TileWalk {
@@ -394,11 +406,12 @@ struct ActTile {
     void* out;                 // bf16, or codes
     uint16_t* preact;          // or NULL
     const uint16_t* residual;  // or NULL; may be out
-    const float* s_bias;       // the tile's bias, in shared memory
+    float* s_bias;             // 32 values of this warp: the block's bias (0 and left alone without one)
     uint32_t t_row;            // accumulator: this warp's lanes, the tile's first column
     uint32_t stg;              // this warp's staging tile (2 KB)
     float inv, s_out;
     int act, out_fmt;
+    bool has_bias;
     int row0, m_end;  // this warp's first row
     int col_first, N, b;
     bool tma_out, tma_z;  // blocks of 32 rows leave by TMA
@@ -481,14 +494,18 @@ __device__ __forceinline__ void act_stage(uint32_t stg, const float (&y)[32], in
 // quarter and to a scheduler), because the epilogue is bound by latency: a
 // block is a chain of TMEM load, MUFU, staging and store, which one warp a
 // scheduler left bare. Each warp stages and stores its own blocks, so that the
-// warps drift apart and overlap; only the bias and the accumulator hand-over
-// bring them together. Per block: z = acc * inv + bias, kept as bf16 if asked
+// warps drift apart and overlap; nothing is shared between them, and no
+// barrier holds them together. Per block: z = acc * inv + bias, kept as bf16 if asked
 // for, then act(z) + residual as bf16, or act(z) as FP8 codes under the output
 // ring's scale (m_out: their amax so far). The residual arrives as 64-byte row
 // pieces (a warp's load covers 8 rows), the first block's before the
 // accumulator is there, and passes through the staging tile, where each
 // thread finds its own row.
 constexpr int kActPhases = 4;
+
+// Blocks of 32 columns that a warp may have in a tile.
+template <int BN>
+constexpr int kActBlocks = (BN / 32 + kActPhases - 1) / kActPhases;
 
 struct ActResidual {
     uint4 v[4];
@@ -505,14 +522,20 @@ struct ActResidual {
     }
 };
 
+// bias: this lane's column of each of the warp's blocks.
 template <int BN, int ACT, bool OUT8>
-__device__ __forceinline__ void act_blocks(const ActTile& t, ActResidual& res, float& m_out, int phase, int lane) {
+__device__ __forceinline__ void act_blocks(const ActTile& t, ActResidual& res, const float (&bias)[kActBlocks<BN>],
+                                           float& m_out, int phase, int lane) {
     const int left = (t.N - t.col_first + 31) / 32;
     const int nch = left < BN / 32 ? left : BN / 32;
 #pragma unroll 1
     for (int c = phase; c < nch; c += kActPhases) {
         const int col0 = t.col_first + c * 32;
         uint32_t acc[32];
+        if (t.has_bias) {
+            __syncwarp();  // the previous block's readers are done
+            t.s_bias[lane] = c < kActPhases ? bias[0] : bias[kActBlocks<BN> - 1];
+        }
         if (t.has) {
             __syncwarp();
             tmem_ld<32>(t.t_row + c * 32, acc);
@@ -521,14 +544,14 @@ __device__ __forceinline__ void act_blocks(const ActTile& t, ActResidual& res, f
 #pragma unroll
             for (int i = 0; i < 32; ++i) acc[i] = 0u;
         }
+        __syncwarp();
         float y[32];
 #pragma unroll
         for (int i = 0; i < 32; i += 4) {
-            const float4 bias = *reinterpret_cast<const float4*>(t.s_bias + c * 32 + i);
-            split(fma2(f2(__uint_as_float(acc[i]), __uint_as_float(acc[i + 1])), f2(t.inv), f2(bias.x, bias.y)), y[i],
-                  y[i + 1]);
-            split(fma2(f2(__uint_as_float(acc[i + 2]), __uint_as_float(acc[i + 3])), f2(t.inv), f2(bias.z, bias.w)),
-                  y[i + 2], y[i + 3]);
+            const float4 v = *reinterpret_cast<const float4*>(t.s_bias + i);
+            split(fma2(f2(__uint_as_float(acc[i]), __uint_as_float(acc[i + 1])), f2(t.inv), f2(v.x, v.y)), y[i], y[i + 1]);
+            split(fma2(f2(__uint_as_float(acc[i + 2]), __uint_as_float(acc[i + 3])), f2(t.inv), f2(v.z, v.w)), y[i + 2],
+                  y[i + 3]);
         }
         if (t.preact) {
             act_stage_free(lane);
@@ -594,15 +617,136 @@ __device__ __forceinline__ void act_blocks(const ActTile& t, ActResidual& res, f
 }
 
 template <int BN, bool OUT8>
-__device__ __forceinline__ void act_tile(const ActTile& t, ActResidual& res, float& m_out, int phase, int lane) {
+__device__ __forceinline__ void act_tile(const ActTile& t, ActResidual& res, const float (&bias)[kActBlocks<BN>],
+                                         float& m_out, int phase, int lane) {
     if (t.row0 >= t.m_end) return;  // no row of this warp exists
     switch (t.act) {
-        case FP8_ACT_NONE: act_blocks<BN, FP8_ACT_NONE, OUT8>(t, res, m_out, phase, lane); break;
-        case FP8_ACT_RELU: act_blocks<BN, FP8_ACT_RELU, OUT8>(t, res, m_out, phase, lane); break;
-        case FP8_ACT_GELU: act_blocks<BN, FP8_ACT_GELU, OUT8>(t, res, m_out, phase, lane); break;
-        case FP8_ACT_GELU_TANH: act_blocks<BN, FP8_ACT_GELU_TANH, OUT8>(t, res, m_out, phase, lane); break;
-        default: act_blocks<BN, FP8_ACT_SILU, OUT8>(t, res, m_out, phase, lane); break;
+        case FP8_ACT_NONE: act_blocks<BN, FP8_ACT_NONE, OUT8>(t, res, bias, m_out, phase, lane); break;
+        case FP8_ACT_RELU: act_blocks<BN, FP8_ACT_RELU, OUT8>(t, res, bias, m_out, phase, lane); break;
+        case FP8_ACT_GELU: act_blocks<BN, FP8_ACT_GELU, OUT8>(t, res, bias, m_out, phase, lane); break;
+        case FP8_ACT_GELU_TANH: act_blocks<BN, FP8_ACT_GELU_TANH, OUT8>(t, res, bias, m_out, phase, lane); break;
+        default: act_blocks<BN, FP8_ACT_SILU, OUT8>(t, res, bias, m_out, phase, lane); break;
     }
+}
+
+// The amax of an FP8 output, over every epilogue thread of the grid: one
+// atomicMax a CTA, then a ticket; the CTA holding the last one folds it into
+// the output's ring. T: epilogue threads of the CTA; red: shared memory that
+// no epilogue thread uses any more after the first barrier.
+template <int T>
+__device__ __forceinline__ void out8_finish(const GemmParams& p, float m_out, float* s_bias, int warp, int lane, int etid) {
+    uint32_t bits = __reduce_max_sync(0xffffffffu, __float_as_uint(m_out));
+    epilogue_bar<T>();  // the bias slots are free now
+    uint32_t* red = reinterpret_cast<uint32_t*>(s_bias);
+    if (lane == 0) red[warp - 2] = bits;
+    epilogue_bar<T>();
+    if (etid != 0) return;
+    bits = red[0];
+    for (int w = 1; w < T / 32; ++w) bits = max(bits, red[w]);
+    fp8_ring* ring = p.out_ring;
+    if (bits != 0u) atomicMax(&ring->amax_bits, bits);
+    const uint32_t ticket = atom_add_acq_rel(&ring->ticket, 1u);
+    if (ticket != gridDim.x - 1) return;
+    volatile fp8_ring* rr = ring;
+    float h[FP8_RING_HISTORY];
+    const uint32_t idx = ring_read(rr, h);
+    const float a = __uint_as_float(atomicExch(&ring->amax_bits, 0u));
+    ring_fold(rr, h, idx, a, fmt_max(p.out_fmt));
+    if (p.out_amax) *p.out_amax = a;
+    rr->ticket = 0u;
+}
+
+// The epilogue role of an activation launch (unswapped tiles). What a tile
+// needs from global memory is asked for one tile early: its bias (a lane
+// fetches a column of each of its warp's blocks), and its residual as a prefetch into L2, whose first block each warp
+// then loads before the accumulator is there.
+template <int BN, int CTAS, bool OUT8>
+__device__ __forceinline__ void act_epilogue(const GemmParams& p, const EpArgs<true>& ep, const CUtensorMap* map_c,
+                                             float* s_bias, uint32_t stg0, uint32_t tmem_base, uint32_t bar_tfull,
+                                             uint32_t bar_tempty, uint32_t rank, int unit0, int unit_step,
+                                             int total_units, const TileWalk& walk, int M, int N, int tma_store,
+                                             int warp, int lane) {
+    constexpr int ET = epi_threads(true, false);
+    griddep_wait();
+    griddep_launch();
+    const int q = warp & 3, phase = (warp - 2) >> 2;
+    const int etid = threadIdx.x - 64;
+    const float bscale = p.bias_kind == 2 ? __ldg(p.bias_scale) : 1.0f;
+    float m_out = 0.0f;
+    ActTile t;
+    t.map_out = map_c;
+    t.map_z = &ep.tz;
+    t.s_bias = s_bias + (warp - 2) * 32;
+    t.s_bias[lane] = 0.0f;
+    t.has_bias = p.bias_kind != 0;
+    t.stg = stg0 + uint32_t(warp - 2) * 2048u;
+    t.inv = (1.0f / __ldg(p.sa)) * (1.0f / __ldg(p.sb));
+    t.s_out = 1.0f;
+    if (OUT8) {  // the ring's scale before this call: the fold waits for every CTA's ticket
+        t.s_out = *reinterpret_cast<volatile float*>(&p.out_ring->scale);
+        if (blockIdx.x == 0 && etid == 0) *p.out_scale = t.s_out;
+    }
+    t.act = ep.act;
+    t.out_fmt = p.out_fmt;
+    t.m_end = M;
+    t.N = N;
+    t.tma_out = t.vec_out = tma_store;
+    t.tma_z = t.vec_z = ep.fast;
+    t.has = true;
+    const bool res_vec = !OUT8 && ep.residual && ep.fast;
+    float bias[kActBlocks<BN>] = {}, bias_next[kActBlocks<BN>] = {};
+    auto ask_bias = [&](int nb) {
+#pragma unroll
+        for (int i = 0; i < kActBlocks<BN>; ++i) {
+            const int col = nb * BN + (phase + i * kActPhases) * 32 + lane;
+            if (col >= N || p.bias_kind == 0) bias_next[i] = 0.0f;
+            else if (p.bias_kind == 1) bias_next[i] = bf16_value(__ldg(static_cast<const uint16_t*>(p.bias) + col));
+            else bias_next[i] = __fdiv_rn(fp8_to_f32(__ldg(static_cast<const uint8_t*>(p.bias) + col), p.bias_fmt), bscale);
+        }
+    };
+    int mb = 0, nb = 0, b = 0;
+    if (unit0 < total_units) {
+        tile_coords(unit0, walk, mb, nb, b);
+        ask_bias(nb);
+    }
+    bool failed = false;
+    int it = 0;
+    for (int u = unit0; u < total_units; u += unit_step, ++it) {
+        const int buf = it & 1;
+        t.row0 = (mb * CTAS + int(rank)) * BM + q * 32;
+        t.col_first = nb * BN;
+        t.b = b;
+        t.out = OUT8 ? static_cast<void*>(reinterpret_cast<uint8_t*>(p.out) + int64_t(b) * p.stride_c)
+                     : static_cast<void*>(p.out + int64_t(b) * p.stride_c);
+        t.preact = ep.preact ? ep.preact + int64_t(b) * p.stride_c : nullptr;
+        t.residual = ep.residual ? ep.residual + int64_t(b) * ep.stride_r : nullptr;
+        ActResidual res;
+        if (res_vec) res.load(t, phase, lane);
+#pragma unroll
+        for (int i = 0; i < kActBlocks<BN>; ++i) bias[i] = bias_next[i];
+        if (u + unit_step < total_units) {
+            tile_coords(u + unit_step, walk, mb, nb, b);
+            ask_bias(nb);
+            const int64_t row = int64_t(mb * CTAS + int(rank)) * BM + q * 32 + lane;
+            if (res_vec && row < M) {
+                const uint16_t* r = ep.residual + int64_t(b) * ep.stride_r + row * N;
+#pragma unroll
+                for (int c = phase * 32; c < BN; c += kActPhases * 32)
+                    if (nb * BN + c < N) asm volatile("prefetch.global.L2 [%0];" ::"l"(r + nb * BN + c));
+            }
+        }
+        if (!failed) failed = !wait_bounded_warp(bar_tfull + 8 * buf, (it >> 1) & 1);
+        if (failed) continue;  // the other warps find it out for themselves
+        tc_fence_after();
+        t.t_row = tmem_base + (uint32_t(q * 32) << 16) + buf * BN;
+        act_tile<BN, OUT8>(t, res, bias, m_out, phase, lane);
+        tc_fence_before();
+        // release the accumulator to the MMA issuer (the pair's leader)
+        if (CTAS == 1) mbar_arrive(bar_tempty + 8 * buf);
+        else           mbar_arrive_cluster(map_to_rank(bar_tempty + 8 * buf, 0));
+    }
+    if (lane == 0) bulk_wait_read<0>();  // the staging tiles outlive the stores that read them
+    if (OUT8) out8_finish<ET>(p, m_out, s_bias, warp, lane, etid);
 }
 
 // One kernel for both tile shapes: CTAS = 1 computes 128 x BN tiles per CTA;
@@ -632,6 +776,9 @@ fp8_gemm_kernel(const __grid_constant__ CUtensorMap tm_a, const __grid_constant_
     static_assert(!GROUP || (CTAS == 1 && !SPLIT && !SWAP && !OUT8), "grouped launches use plain one-SM tiles");
     extern __shared__ __align__(1024) uint8_t smem_raw[];
     uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
+    if constexpr (L::kAct) {
+        if (!smem_fits<L>(smem_raw, smem)) return;
+    }
     const uint32_t s_base = smem_addr(smem);
     const uint32_t s_a = s_base;
     const uint32_t s_b = s_base + STAGES * L::kABytes;
@@ -865,444 +1012,386 @@ fp8_gemm_kernel(const __grid_constant__ CUtensorMap tm_a, const __grid_constant_
         }
     } else {
         // ----------------------------------------------------- epilogue ---
-        griddep_wait();
-        griddep_launch();
-        const int q = warp & 3;             // TMEM lane quarter this warp may access
-        const int row_in_tile = q * 32 + lane;
-        const int etid = threadIdx.x - 64;  // 0 .. ET-1
-        const bool store_lead = etid == 0;  // issues the TMA stores
-        const uint32_t stg0 = s_base + L::kStgOffset;
-        int n_st = 0;  // TMA stores issued so far (they take the staging tiles in turn)
-        float inv = (1.0f / __ldg(p.sa)) * (1.0f / __ldg(p.sb));
-        int bias_kind = p.bias_kind, bias_fmt = p.bias_fmt;
-        const void* bias_ptr = p.bias;
-        float bscale = (HAS_BIAS && bias_kind == 2) ? __ldg(p.bias_scale) : 1.0f;
-        uint16_t* out_base = p.out;
-        const CUtensorMap* map_c = &tm_c;
-        // FP8 output: the ring's scale before this call (every CTA reads it
-        // before any CTA can fold: the fold waits for all CTAs' tickets)
-        float s_out = 1.0f, m_out = 0.0f;
-        if (OUT8) {
-            s_out = *reinterpret_cast<volatile float*>(&p.out_ring->scale);
-            if (blockIdx.x == 0 && etid == 0) *p.out_scale = s_out;
-        }
-        bool failed = false;
-        int it = 0;
-        for (int u = unit0; u < total_units; u = unit_of<GROUP>(++it, unit0, unit_step)) {
-            int t = u / split;
-            const int split_id = u - t * split;
-            TileWalk w = walk;
-            int ebn = BN, n_base = 0;  // the unit's tile width and first column
-            if constexpr (GROUP) {
-                const GroupProblem& q = group_problem(grp, u, t);
-                w = {q.m_tiles, q.n_tiles, walk.group_m};
-                ebn = q.bn;
-                n_base = q.n_base;
-                M = q.M;
-                N = q.N;
-                tma_store = q.tma_store;
-                vec_store = q.vec_store;
-                map_c = &q.tc;
-                out_base = q.out;
-                bias_kind = q.bias_kind;
-                bias_fmt = q.bias_fmt;
-                bias_ptr = q.bias;
-                inv = (1.0f / __ldg(q.sa)) * (1.0f / __ldg(q.sb));
-                bscale = (HAS_BIAS && bias_kind == 2) ? __ldg(q.bias_scale) : 1.0f;
+        if constexpr (EP && !SWAP) {
+            act_epilogue<BN, CTAS, OUT8>(p, ep, &tm_c, s_bias, s_base + L::kStgOffset, tmem_base, bar_tfull, bar_tempty, rank,
+                                         unit0, unit_step, total_units, walk, M, N, tma_store, warp, lane);
+        } else {
+            griddep_wait();
+            griddep_launch();
+            const int q = warp & 3;             // TMEM lane quarter this warp may access
+            const int row_in_tile = q * 32 + lane;
+            const int etid = threadIdx.x - 64;  // 0 .. kEpiThreads-1
+            const bool store_lead = etid == 0;  // issues the TMA stores
+            const uint32_t stg0 = s_base + L::kStgOffset;
+            int n_st = 0;  // TMA stores issued so far (they take the staging tiles in turn)
+            float inv = (1.0f / __ldg(p.sa)) * (1.0f / __ldg(p.sb));
+            int bias_kind = p.bias_kind, bias_fmt = p.bias_fmt;
+            const void* bias_ptr = p.bias;
+            float bscale = (HAS_BIAS && bias_kind == 2) ? __ldg(p.bias_scale) : 1.0f;
+            uint16_t* out_base = p.out;
+            const CUtensorMap* map_c = &tm_c;
+            // FP8 output: the ring's scale before this call (every CTA reads it
+            // before any CTA can fold: the fold waits for all CTAs' tickets)
+            float s_out = 1.0f, m_out = 0.0f;
+            if (OUT8) {
+                s_out = *reinterpret_cast<volatile float*>(&p.out_ring->scale);
+                if (blockIdx.x == 0 && etid == 0) *p.out_scale = s_out;
             }
-            int mb, nb, b;
-            tile_coords(t, w, mb, nb, b);
-            const int buf = it & 1;
-            const uint32_t acc_phase = (it >> 1) & 1;
-            const int m0 = mb * BM * CTAS + int(rank) * BM;  // this CTA's first output row
-            auto bias_at = [&](int col) {
-                float v = 0.0f;
-                if (col < N && bias_kind != 0) {  // a grouped launch may mix problems with and without bias
-                    if (bias_kind == 1) {
-                        v = __uint_as_float(uint32_t(__ldg(static_cast<const uint16_t*>(bias_ptr) + col)) << 16);
-                    } else {
-                        v = __fdiv_rn(fp8_to_f32(__ldg(static_cast<const uint8_t*>(bias_ptr) + col), bias_fmt),
-                                      bscale);
-                    }
+            bool failed = false;
+            int it = 0;
+            for (int u = unit0; u < total_units; u = unit_of<GROUP>(++it, unit0, unit_step)) {
+                int t = u / split;
+                const int split_id = u - t * split;
+                TileWalk w = walk;
+                int ebn = BN, n_base = 0;  // the unit's tile width and first column
+                if constexpr (GROUP) {
+                    const GroupProblem& q = group_problem(grp, u, t);
+                    w = {q.m_tiles, q.n_tiles, walk.group_m};
+                    ebn = q.bn;
+                    n_base = q.n_base;
+                    M = q.M;
+                    N = q.N;
+                    tma_store = q.tma_store;
+                    vec_store = q.vec_store;
+                    map_c = &q.tc;
+                    out_base = q.out;
+                    bias_kind = q.bias_kind;
+                    bias_fmt = q.bias_fmt;
+                    bias_ptr = q.bias;
+                    inv = (1.0f / __ldg(q.sa)) * (1.0f / __ldg(q.sb));
+                    bscale = (HAS_BIAS && bias_kind == 2) ? __ldg(q.bias_scale) : 1.0f;
                 }
-                return v;
-            };
-            if (HAS_BIAS && !SWAP && !EP) {
-                // the tile's BN bias values, dequantized once into shared memory
-                epilogue_bar();  // the previous tile's readers are done
-                for (int j = etid; j < ebn; j += kEpiThreads) s_bias[j] = bias_at(n_base + nb * ebn + j);
-                epilogue_bar();
-            }
-            // an activation epilogue fetches its bias (a column a thread) and its
-            // first residual block while the accumulator is still being made
-            const int phase = (warp - 2) >> 2;
-            float bias_v = 0.0f;
-            ActTile at;
-            ActResidual res;
-            if constexpr (EP && !SWAP) {
-                static_assert(ET >= BN, "a bias column a thread");
-                if (etid < BN) bias_v = bias_at(nb * BN + etid);
-                at.map_out = &tm_c;
-                at.map_z = &ep.tz;
-                at.out = OUT8 ? static_cast<void*>(reinterpret_cast<uint8_t*>(p.out) + int64_t(b) * p.stride_c)
-                              : static_cast<void*>(p.out + int64_t(b) * p.stride_c);
-                at.preact = ep.preact ? ep.preact + int64_t(b) * p.stride_c : nullptr;
-                at.residual = ep.residual ? ep.residual + int64_t(b) * ep.stride_r : nullptr;
-                at.s_bias = s_bias;
-                at.stg = stg0 + uint32_t(warp - 2) * 2048u;
-                at.inv = inv;
-                at.s_out = s_out;
-                at.act = ep.act;
-                at.out_fmt = p.out_fmt;
-                at.row0 = m0 + q * 32;
-                at.m_end = M;
-                at.col_first = nb * BN;
-                at.N = N;
-                at.b = b;
-                at.tma_out = at.vec_out = tma_store;
-                at.tma_z = at.vec_z = ep.fast;
-                at.has = true;
-                if (!OUT8 && at.residual && ep.fast) res.load(at, phase, lane);
-            }
-            // every lane waits, then all epilogue warps agree (and each warp
-            // reconverges) before the warp-collective TMEM loads. After a wait
-            // gave up, they all keep walking the units without waiting, so that
-            // they still meet at every named barrier.
-            if (!failed) failed = !wait_bounded(bar_tfull + 8 * buf, acc_phase);
-            failed = epilogue_bar_or<ET>(failed);  // the previous tile's readers are done, too
-            if (failed) continue;
-            if constexpr (EP && !SWAP) {
-                if (etid < BN) s_bias[etid] = bias_v;
-                epilogue_bar<ET>();
-            }
-            tc_fence_after();
-            const uint32_t t_row = tmem_base + (uint32_t(q * 32) << 16) + buf * BN;
-            // Split K: the unit that arrives last at its tile finishes it; the
-            // others leave their fp32 partial in the workspace. Slot layout:
-            // 16-byte piece v of CW-column chunk c of tile row r sits at
-            // ((c * CW / 4 + v) * 128 + r) * 16, so each store and load
-            // instruction of a warp covers 512 contiguous bytes.
-            constexpr int CW = SWAP ? 16 : 32;  // accumulator columns per TMEM load
-            const float4* slots = nullptr;
-            if (SPLIT && split > 1 && csplit) {
-                // cluster split: CTA r of the cluster is split r of the tile
-                // (one tile per cluster); splits 1.. push their partials into
-                // split 0's staging area (free in swapped launches), slot r - 1,
-                // laid out as the workspace's slots, and arrive on its barrier
-                if (split_id != 0) {
-                    const uint32_t dst = map_to_rank(stg0 + uint32_t(split_id - 1) * (BM * BN * 4), 0);
-#pragma unroll 1
-                    for (int c = 0; c < BN / CW; ++c) {
-                        if (nb * BN + c * CW >= N) break;  // uniform; split 0 skips it too
-                        uint32_t r[CW];
-                        tmem_ld<CW>(t_row + c * CW, r);
-                        tmem_ld_wait();
-#pragma unroll
-                        for (int v = 0; v < CW / 4; ++v)
-                            st_cluster_v4(dst + uint32_t(((c * (CW / 4) + v) * 128 + row_in_tile) * 16),
-                                          __uint_as_float(r[4 * v]), __uint_as_float(r[4 * v + 1]),
-                                          __uint_as_float(r[4 * v + 2]), __uint_as_float(r[4 * v + 3]));
+                int mb, nb, b;
+                tile_coords(t, w, mb, nb, b);
+                const int buf = it & 1;
+                const uint32_t acc_phase = (it >> 1) & 1;
+                const int m0 = mb * BM * CTAS + int(rank) * BM;  // this CTA's first output row
+                if (HAS_BIAS && !SWAP) {
+                    // the tile's BN bias values, dequantized once into shared memory
+                    epilogue_bar();  // the previous tile's readers are done
+                    for (int j = etid; j < ebn; j += kEpiThreads) {
+                        const int col = n_base + nb * ebn + j;
+                        float v = 0.0f;
+                        if (col < N && bias_kind != 0) {  // a grouped launch may mix problems with and without bias
+                            if (bias_kind == 1) {
+                                v = __uint_as_float(uint32_t(__ldg(static_cast<const uint16_t*>(bias_ptr) + col)) << 16);
+                            } else {
+                                v = __fdiv_rn(fp8_to_f32(__ldg(static_cast<const uint8_t*>(bias_ptr) + col), bias_fmt),
+                                              bscale);
+                            }
+                        }
+                        s_bias[j] = v;
                     }
-                    mbar_arrive_cluster(map_to_rank(bar_red, 0));  // release: the stores above come first
-                    tc_fence_before();
-                    mbar_arrive(bar_tempty + 8 * buf);
-                    continue;
+                    epilogue_bar();
                 }
-                if (!failed) failed = !wait_bounded_cluster(bar_red, 0);
+                // every lane waits, then all epilogue warps agree (and each warp
+                // reconverges) before the warp-collective TMEM loads. After a wait
+                // gave up, they all keep walking the units without waiting, so that
+                // they still meet at every named barrier.
+                if (!failed) failed = !wait_bounded(bar_tfull + 8 * buf, acc_phase);
                 failed = epilogue_bar_or(failed);
                 if (failed) continue;
-            } else if (SPLIT && split > 1) {
-                uint32_t* cnt = p.ws_cnt + 2 * (t * CTAS + int(rank));
-                slots = reinterpret_cast<const float4*>(p.ws) + size_t(t * CTAS + int(rank)) * split * (BM * BN / 4);
-                if (etid == 0) *ticket_slot = atomicAdd(cnt, 1u);
-                epilogue_bar();
-                const bool last = *ticket_slot == uint32_t(split - 1);
-                if (!last) {
-                    float4* mine = const_cast<float4*>(slots) + size_t(split_id) * (BM * BN / 4);
+                tc_fence_after();
+                const uint32_t t_row = tmem_base + (uint32_t(q * 32) << 16) + buf * BN;
+                // Split K: the unit that arrives last at its tile finishes it; the
+                // others leave their fp32 partial in the workspace. Slot layout:
+                // 16-byte piece v of CW-column chunk c of tile row r sits at
+                // ((c * CW / 4 + v) * 128 + r) * 16, so each store and load
+                // instruction of a warp covers 512 contiguous bytes.
+                constexpr int CW = SWAP ? 16 : 32;  // accumulator columns per TMEM load
+                const float4* slots = nullptr;
+                if (SPLIT && split > 1 && csplit) {
+                    // cluster split: CTA r of the cluster is split r of the tile
+                    // (one tile per cluster); splits 1.. push their partials into
+                    // split 0's staging area (free in swapped launches), slot r - 1,
+                    // laid out as the workspace's slots, and arrive on its barrier
+                    if (split_id != 0) {
+                        const uint32_t dst = map_to_rank(stg0 + uint32_t(split_id - 1) * (BM * BN * 4), 0);
 #pragma unroll 1
-                    for (int c = 0; c < BN / CW; ++c) {
-                        if (nb * BN + c * CW >= N) break;  // uniform; the finisher skips it too
-                        uint32_t r[CW];
-                        tmem_ld<CW>(t_row + c * CW, r);
-                        tmem_ld_wait();
+                        for (int c = 0; c < BN / CW; ++c) {
+                            if (nb * BN + c * CW >= N) break;  // uniform; split 0 skips it too
+                            uint32_t r[CW];
+                            tmem_ld<CW>(t_row + c * CW, r);
+                            tmem_ld_wait();
 #pragma unroll
-                        for (int v = 0; v < CW / 4; ++v)
-                            __stcg(mine + (c * (CW / 4) + v) * 128 + row_in_tile,
-                                   make_float4(__uint_as_float(r[4 * v]), __uint_as_float(r[4 * v + 1]),
-                                               __uint_as_float(r[4 * v + 2]), __uint_as_float(r[4 * v + 3])));
+                            for (int v = 0; v < CW / 4; ++v)
+                                st_cluster_v4(dst + uint32_t(((c * (CW / 4) + v) * 128 + row_in_tile) * 16),
+                                              __uint_as_float(r[4 * v]), __uint_as_float(r[4 * v + 1]),
+                                              __uint_as_float(r[4 * v + 2]), __uint_as_float(r[4 * v + 3]));
+                        }
+                        mbar_arrive_cluster(map_to_rank(bar_red, 0));  // release: the stores above come first
+                        tc_fence_before();
+                        mbar_arrive(bar_tempty + 8 * buf);
+                        continue;
                     }
-                    __threadfence();
+                    if (!failed) failed = !wait_bounded_cluster(bar_red, 0);
+                    failed = epilogue_bar_or(failed);
+                    if (failed) continue;
+                } else if (SPLIT && split > 1) {
+                    uint32_t* cnt = p.ws_cnt + 2 * (t * CTAS + int(rank));
+                    slots = reinterpret_cast<const float4*>(p.ws) + size_t(t * CTAS + int(rank)) * split * (BM * BN / 4);
+                    if (etid == 0) *ticket_slot = atomicAdd(cnt, 1u);
                     epilogue_bar();
-                    if (etid == 0) red_release_add(cnt + 1, 1u);
-                    tc_fence_before();
-                    if (CTAS == 1) mbar_arrive(bar_tempty + 8 * buf);
-                    else           mbar_arrive_cluster(map_to_rank(bar_tempty + 8 * buf, 0));
-                    continue;
-                }
-                if (etid == 0) {
-                    wait_count(cnt + 1, uint32_t(split - 1));
-                    cnt[0] = 0u;  // the tile's counters are ready for the next call
-                    cnt[1] = 0u;
-                }
-                epilogue_bar();
-            }
-            const int row = m0 + row_in_tile;
-            // swapped operands: this thread's TMEM lane is output column `row`
-            // of C (the kernel's M is C's N), its accumulator columns are C's rows
-            float bias_row = 0.0f;
-            if (SWAP && HAS_BIAS && row < M && (!EP || bias_kind != 0)) {
-                if (bias_kind == 1)
-                    bias_row = __uint_as_float(uint32_t(__ldg(static_cast<const uint16_t*>(bias_ptr) + row)) << 16);
-                else
-                    bias_row = __fdiv_rn(fp8_to_f32(__ldg(static_cast<const uint8_t*>(bias_ptr) + row), bias_fmt),
-                                         bscale);
-            }
-            uint16_t* orow = SWAP ? out_base + int64_t(b) * p.stride_c + row
-                                  : out_base + int64_t(b) * p.stride_c + int64_t(row) * N;
-            if constexpr (EP && !SWAP) {
-                at.t_row = t_row;
-                act_tile<BN, OUT8>(at, res, m_out, phase, lane);
-            }
-            if constexpr (!EP && !SPLIT && !SWAP && !OUT8) {
-                if (tma_store) {
-                    // The common case, pipelined: chunk c + 1's accumulator
-                    // columns leave TMEM while chunk c is converted, staged and
-                    // stored (two register sets, the wait tied to the set it
-                    // waits for).
-                    const int col_first = n_base + nb * ebn;
-                    const int left = (N - col_first + 31) / 32;
-                    const int nch = left < ebn / 32 ? left : ebn / 32;
-                    auto emit = [&](const uint32_t (&r)[32], int c) {
-                        float y[32];
+                    const bool last = *ticket_slot == uint32_t(split - 1);
+                    if (!last) {
+                        float4* mine = const_cast<float4*>(slots) + size_t(split_id) * (BM * BN / 4);
+#pragma unroll 1
+                        for (int c = 0; c < BN / CW; ++c) {
+                            if (nb * BN + c * CW >= N) break;  // uniform; the finisher skips it too
+                            uint32_t r[CW];
+                            tmem_ld<CW>(t_row + c * CW, r);
+                            tmem_ld_wait();
 #pragma unroll
-                        for (int i = 0; i < 32; ++i) {
-                            const float bias = HAS_BIAS ? s_bias[c * 32 + i] : 0.0f;
-                            y[i] = fmaf(__uint_as_float(r[i]), inv, bias);
+                            for (int v = 0; v < CW / 4; ++v)
+                                __stcg(mine + (c * (CW / 4) + v) * 128 + row_in_tile,
+                                       make_float4(__uint_as_float(r[4 * v]), __uint_as_float(r[4 * v + 1]),
+                                                   __uint_as_float(r[4 * v + 2]), __uint_as_float(r[4 * v + 3])));
                         }
-                        stage_and_store<L>(stg0, n_st, row_in_tile, y, store_lead, map_c, col_first + c * 32, m0, b);
-                        ++n_st;
-                    };
-                    uint32_t ra[32], rb[32];
-                    tmem_ld<32>(t_row, ra);
-                    tmem_ld_wait_tied(ra);
-#pragma unroll 1
-                    for (int c = 0; c < nch; c += 2) {
-                        __syncwarp();
-                        if (c + 1 < nch) tmem_ld<32>(t_row + (c + 1) * 32, rb);
-                        emit(ra, c);
-                        if (c + 1 >= nch) break;
-                        tmem_ld_wait_tied(rb);
-                        __syncwarp();
-                        if (c + 2 < nch) tmem_ld<32>(t_row + (c + 2) * 32, ra);
-                        emit(rb, c + 1);
-                        if (c + 2 < nch) tmem_ld_wait_tied(ra);
+                        __threadfence();
+                        epilogue_bar();
+                        if (etid == 0) red_release_add(cnt + 1, 1u);
+                        tc_fence_before();
+                        if (CTAS == 1) mbar_arrive(bar_tempty + 8 * buf);
+                        else           mbar_arrive_cluster(map_to_rank(bar_tempty + 8 * buf, 0));
+                        continue;
                     }
-                    tc_fence_before();
-                    if (CTAS == 1) mbar_arrive(bar_tempty + 8 * buf);
-                    else           mbar_arrive_cluster(map_to_rank(bar_tempty + 8 * buf, 0));
-                    continue;
+                    if (etid == 0) {
+                        wait_count(cnt + 1, uint32_t(split - 1));
+                        cnt[0] = 0u;  // the tile's counters are ready for the next call
+                        cnt[1] = 0u;
+                    }
+                    epilogue_bar();
                 }
-            }
-            // an activation epilogue is done here; a swapped one is part of the loop
-            const int n_chunks = EP && !SWAP ? 0 : ebn / CW;
-#pragma unroll 1
-            for (int c = 0; c < n_chunks; ++c) {
-                const int col0 = n_base + nb * ebn + c * CW;
-                if (col0 >= N) break;  // uniform over the epilogue warps
-                uint32_t r[CW];
-                tmem_ld<CW>(t_row + c * CW, r);
-                tmem_ld_wait();
-                if (SPLIT && split > 1) {
-                    // the sum over the splits in split order, whatever order
-                    // they arrived in (the result does not depend on timing)
-                    float acc[CW];
-#pragma unroll 1
-                    for (int sp = 0; sp < split; ++sp) {
-                        if (sp == split_id) {
+                const int row = m0 + row_in_tile;
+                // swapped operands: this thread's TMEM lane is output column `row`
+                // of C (the kernel's M is C's N), its accumulator columns are C's rows
+                float bias_row = 0.0f;
+                if (SWAP && HAS_BIAS && row < M && (!EP || bias_kind != 0)) {
+                    if (bias_kind == 1)
+                        bias_row = __uint_as_float(uint32_t(__ldg(static_cast<const uint16_t*>(bias_ptr) + row)) << 16);
+                    else
+                        bias_row = __fdiv_rn(fp8_to_f32(__ldg(static_cast<const uint8_t*>(bias_ptr) + row), bias_fmt),
+                                             bscale);
+                }
+                uint16_t* orow = SWAP ? out_base + int64_t(b) * p.stride_c + row
+                                      : out_base + int64_t(b) * p.stride_c + int64_t(row) * N;
+                if constexpr (!SPLIT && !SWAP && !OUT8) {
+                    if (tma_store) {
+                        // The common case, pipelined: chunk c + 1's accumulator
+                        // columns leave TMEM while chunk c is converted, staged and
+                        // stored (two register sets, the wait tied to the set it
+                        // waits for).
+                        const int col_first = n_base + nb * ebn;
+                        const int left = (N - col_first + 31) / 32;
+                        const int nch = left < ebn / 32 ? left : ebn / 32;
+                        auto emit = [&](const uint32_t (&r)[32], int c) {
+                            float y[32];
 #pragma unroll
-                            for (int i = 0; i < CW; ++i)
-                                acc[i] = sp == 0 ? __uint_as_float(r[i]) : acc[i] + __uint_as_float(r[i]);
-                        } else if (csplit) {
-                            const uint32_t src = stg0 + uint32_t(sp - 1) * (BM * BN * 4) +
-                                                 uint32_t(((c * (CW / 4)) * 128 + row_in_tile) * 16);
-#pragma unroll
-                            for (int v = 0; v < CW / 4; ++v) {
-                                float4 x;
-                                asm volatile("ld.shared.v4.f32 {%0, %1, %2, %3}, [%4];"
-                                             : "=f"(x.x), "=f"(x.y), "=f"(x.z), "=f"(x.w)
-                                             : "r"(src + uint32_t(v * 128 * 16)));
-                                acc[4 * v] = acc[4 * v] + x.x;
-                                acc[4 * v + 1] = acc[4 * v + 1] + x.y;
-                                acc[4 * v + 2] = acc[4 * v + 2] + x.z;
-                                acc[4 * v + 3] = acc[4 * v + 3] + x.w;
+                            for (int i = 0; i < 32; ++i) {
+                                const float bias = HAS_BIAS ? s_bias[c * 32 + i] : 0.0f;
+                                y[i] = fmaf(__uint_as_float(r[i]), inv, bias);
                             }
-                        } else {
-                            const float4* src =
-                                slots + size_t(sp) * (BM * BN / 4) + c * (CW / 4) * 128 + row_in_tile;
+                            stage_and_store<L>(stg0, n_st, row_in_tile, y, store_lead, map_c, col_first + c * 32, m0, b);
+                            ++n_st;
+                        };
+                        uint32_t ra[32], rb[32];
+                        tmem_ld<32>(t_row, ra);
+                        tmem_ld_wait_tied(ra);
+#pragma unroll 1
+                        for (int c = 0; c < nch; c += 2) {
+                            __syncwarp();
+                            if (c + 1 < nch) tmem_ld<32>(t_row + (c + 1) * 32, rb);
+                            emit(ra, c);
+                            if (c + 1 >= nch) break;
+                            tmem_ld_wait_tied(rb);
+                            __syncwarp();
+                            if (c + 2 < nch) tmem_ld<32>(t_row + (c + 2) * 32, ra);
+                            emit(rb, c + 1);
+                            if (c + 2 < nch) tmem_ld_wait_tied(ra);
+                        }
+                        tc_fence_before();
+                        if (CTAS == 1) mbar_arrive(bar_tempty + 8 * buf);
+                        else           mbar_arrive_cluster(map_to_rank(bar_tempty + 8 * buf, 0));
+                        continue;
+                    }
+                }
+#pragma unroll 1
+                for (int c = 0; c < ebn / CW; ++c) {
+                    const int col0 = n_base + nb * ebn + c * CW;
+                    if (col0 >= N) break;  // uniform over the epilogue warps
+                    uint32_t r[CW];
+                    tmem_ld<CW>(t_row + c * CW, r);
+                    tmem_ld_wait();
+                    if (SPLIT && split > 1) {
+                        // the sum over the splits in split order, whatever order
+                        // they arrived in (the result does not depend on timing)
+                        float acc[CW];
+#pragma unroll 1
+                        for (int sp = 0; sp < split; ++sp) {
+                            if (sp == split_id) {
 #pragma unroll
-                            for (int v = 0; v < CW / 4; ++v) {
-                                const float4 x = __ldcg(src + v * 128);
-                                acc[4 * v] = sp == 0 ? x.x : acc[4 * v] + x.x;
-                                acc[4 * v + 1] = sp == 0 ? x.y : acc[4 * v + 1] + x.y;
-                                acc[4 * v + 2] = sp == 0 ? x.z : acc[4 * v + 2] + x.z;
-                                acc[4 * v + 3] = sp == 0 ? x.w : acc[4 * v + 3] + x.w;
+                                for (int i = 0; i < CW; ++i)
+                                    acc[i] = sp == 0 ? __uint_as_float(r[i]) : acc[i] + __uint_as_float(r[i]);
+                            } else if (csplit) {
+                                const uint32_t src = stg0 + uint32_t(sp - 1) * (BM * BN * 4) +
+                                                     uint32_t(((c * (CW / 4)) * 128 + row_in_tile) * 16);
+#pragma unroll
+                                for (int v = 0; v < CW / 4; ++v) {
+                                    float4 x;
+                                    asm volatile("ld.shared.v4.f32 {%0, %1, %2, %3}, [%4];"
+                                                 : "=f"(x.x), "=f"(x.y), "=f"(x.z), "=f"(x.w)
+                                                 : "r"(src + uint32_t(v * 128 * 16)));
+                                    acc[4 * v] = acc[4 * v] + x.x;
+                                    acc[4 * v + 1] = acc[4 * v + 1] + x.y;
+                                    acc[4 * v + 2] = acc[4 * v + 2] + x.z;
+                                    acc[4 * v + 3] = acc[4 * v + 3] + x.w;
+                                }
+                            } else {
+                                const float4* src =
+                                    slots + size_t(sp) * (BM * BN / 4) + c * (CW / 4) * 128 + row_in_tile;
+#pragma unroll
+                                for (int v = 0; v < CW / 4; ++v) {
+                                    const float4 x = __ldcg(src + v * 128);
+                                    acc[4 * v] = sp == 0 ? x.x : acc[4 * v] + x.x;
+                                    acc[4 * v + 1] = sp == 0 ? x.y : acc[4 * v + 1] + x.y;
+                                    acc[4 * v + 2] = sp == 0 ? x.z : acc[4 * v + 2] + x.z;
+                                    acc[4 * v + 3] = sp == 0 ? x.w : acc[4 * v + 3] + x.w;
+                                }
                             }
                         }
-                    }
 #pragma unroll
-                    for (int i = 0; i < CW; ++i) r[i] = __float_as_uint(acc[i]);
-                }
-                if constexpr (SWAP) {
-                    // C[col0 + i][row]: lanes hold consecutive columns, so each
-                    // store instruction of a warp writes 64 contiguous bytes
-                    if constexpr (EP) {
-                        // the same, through the activation: z to preact, act(z) + residual to out
+                        for (int i = 0; i < CW; ++i) r[i] = __float_as_uint(acc[i]);
+                    }
+                    if constexpr (SWAP) {
+                        // C[col0 + i][row]: lanes hold consecutive columns, so each
+                        // store instruction of a warp writes 64 contiguous bytes
+                        if constexpr (EP) {
+                            // the same, through the activation: z to preact, act(z) + residual to out
+                            float y[CW];
+#pragma unroll
+                            for (int i = 0; i < CW; ++i) y[i] = fmaf(__uint_as_float(r[i]), inv, bias_row);
+                            if (row < M) {
+                                if (ep.preact) {
+                                    uint16_t* z = ep.preact + (orow - out_base);
+#pragma unroll
+                                    for (int i = 0; i < CW; ++i)
+                                        if (col0 + i < N) z[int64_t(col0 + i) * M] = bf16_bits(y[i]);
+                                }
+                                act_apply(ep.act, y);
+                                if (ep.residual) {
+                                    const uint16_t* res = ep.residual + int64_t(b) * ep.stride_r + row;
+#pragma unroll
+                                    for (int i = 0; i < CW; ++i)
+                                        if (col0 + i < N) y[i] += bf16_value(res[int64_t(col0 + i) * M]);
+                                }
+#pragma unroll
+                                for (int i = 0; i < CW; ++i)
+                                    if (col0 + i < N) orow[int64_t(col0 + i) * M] = bf16_bits(y[i]);
+                            }
+                        } else if (row < M) {
+#pragma unroll
+                            for (int i = 0; i < CW; ++i) {
+                                if (col0 + i >= N) break;
+                                const float y = fmaf(__uint_as_float(r[i]), inv, bias_row);
+                                uint16_t h;
+                                asm("cvt.rn.bf16.f32 %0, %1;" : "=h"(h) : "f"(y));
+                                orow[int64_t(col0 + i) * M] = h;
+                            }
+                        }
+                    } else {
                         float y[CW];
 #pragma unroll
-                        for (int i = 0; i < CW; ++i) y[i] = fmaf(__uint_as_float(r[i]), inv, bias_row);
-                        if (row < M) {
-                            if (ep.preact) {
-                                uint16_t* z = ep.preact + (orow - out_base);
-#pragma unroll
-                                for (int i = 0; i < CW; ++i)
-                                    if (col0 + i < N) z[int64_t(col0 + i) * M] = bf16_bits(y[i]);
-                            }
-                            act_apply(ep.act, y);
-                            if (ep.residual) {
-                                const uint16_t* res = ep.residual + int64_t(b) * ep.stride_r + row;
-#pragma unroll
-                                for (int i = 0; i < CW; ++i)
-                                    if (col0 + i < N) y[i] += bf16_value(res[int64_t(col0 + i) * M]);
-                            }
-#pragma unroll
-                            for (int i = 0; i < CW; ++i)
-                                if (col0 + i < N) orow[int64_t(col0 + i) * M] = bf16_bits(y[i]);
-                        }
-                    } else if (row < M) {
-#pragma unroll
                         for (int i = 0; i < CW; ++i) {
-                            if (col0 + i >= N) break;
-                            const float y = fmaf(__uint_as_float(r[i]), inv, bias_row);
-                            uint16_t h;
-                            asm("cvt.rn.bf16.f32 %0, %1;" : "=h"(h) : "f"(y));
-                            orow[int64_t(col0 + i) * M] = h;
+                            const float bias = HAS_BIAS ? s_bias[c * CW + i] : 0.0f;
+                            y[i] = fmaf(__uint_as_float(r[i]), inv, bias);
                         }
-                    }
-                } else {
-                    float y[CW];
+                        if constexpr (OUT8) {
+                            // q = sat_rne(fp32(y * s_out)); the amax is over the
+                            // unquantized y of this call's own outputs only
+                            if (row < M) {
+                                uint32_t w[8];
 #pragma unroll
-                    for (int i = 0; i < CW; ++i) {
-                        const float bias = HAS_BIAS ? s_bias[c * CW + i] : 0.0f;
-                        y[i] = fmaf(__uint_as_float(r[i]), inv, bias);
-                    }
-                    if constexpr (OUT8) {
-                        // q = sat_rne(fp32(y * s_out)); the amax is over the
-                        // unquantized y of this call's own outputs only
-                        if (row < M) {
-                            uint32_t w[8];
+                                for (int j = 0; j < 8; ++j) {
 #pragma unroll
-                            for (int j = 0; j < 8; ++j) {
+                                    for (int k = 0; k < 4; ++k)
+                                        if (col0 + 4 * j + k < N) m_out = fmaxf(m_out, fabsf(y[4 * j + k]));
+                                    w[j] = cvt_fp8x2(p.out_fmt, __fmul_rn(y[4 * j], s_out), __fmul_rn(y[4 * j + 1], s_out)) |
+                                           (cvt_fp8x2(p.out_fmt, __fmul_rn(y[4 * j + 2], s_out),
+                                                      __fmul_rn(y[4 * j + 3], s_out)) << 16);
+                                }
+                                uint8_t* dst = reinterpret_cast<uint8_t*>(out_base) + int64_t(b) * p.stride_c +
+                                               int64_t(row) * N + col0;
+                                if (vec_store && col0 + 32 <= N) {
+                                    reinterpret_cast<uint4*>(dst)[0] = make_uint4(w[0], w[1], w[2], w[3]);
+                                    reinterpret_cast<uint4*>(dst)[1] = make_uint4(w[4], w[5], w[6], w[7]);
+                                } else {
 #pragma unroll
-                                for (int k = 0; k < 4; ++k)
-                                    if (col0 + 4 * j + k < N) m_out = fmaxf(m_out, fabsf(y[4 * j + k]));
-                                w[j] = cvt_fp8x2(p.out_fmt, __fmul_rn(y[4 * j], s_out), __fmul_rn(y[4 * j + 1], s_out)) |
-                                       (cvt_fp8x2(p.out_fmt, __fmul_rn(y[4 * j + 2], s_out),
-                                                  __fmul_rn(y[4 * j + 3], s_out)) << 16);
+                                    for (int i = 0; i < 32; ++i)
+                                        if (col0 + i < N) dst[i] = uint8_t(w[i >> 2] >> (8 * (i & 3)));
+                                }
                             }
-                            uint8_t* dst = reinterpret_cast<uint8_t*>(out_base) + int64_t(b) * p.stride_c +
-                                           int64_t(row) * N + col0;
+                        } else if (tma_store) {
+                            // the 128 x 32 bf16 block goes to the staging tile whose last
+                            // store is known to have read it (64-byte swizzle: 16-byte
+                            // piece j of row r at (j ^ (r / 2 mod 4)) * 16, so the 8
+                            // lanes of a store phase hit distinct banks); then one TMA
+                            // store, which clips the M / N tails of the output
+                            const uint32_t stg = stg0 + uint32_t(n_st % L::kStgBufs) * L::kStgBytes;
+#pragma unroll
+                            for (int j = 0; j < 4; ++j) {
+                                const uint32_t addr = stg + row_in_tile * 64 + ((j ^ ((row_in_tile >> 1) & 3)) << 4);
+                                asm volatile("st.shared.v4.b32 [%0], {%1, %2, %3, %4};" ::"r"(addr),
+                                             "r"(pack_bf16x2(y[8 * j + 0], y[8 * j + 1])),
+                                             "r"(pack_bf16x2(y[8 * j + 2], y[8 * j + 3])),
+                                             "r"(pack_bf16x2(y[8 * j + 4], y[8 * j + 5])),
+                                             "r"(pack_bf16x2(y[8 * j + 6], y[8 * j + 7]))
+                                             : "memory");
+                            }
+                            fence_proxy_async_smem();
+                            // the store two blocks back has read its tile, which the next
+                            // block reuses (only the newest store may still be reading);
+                            // the barrier publishes that and this block
+                            if (store_lead) bulk_wait_read<L::kStgPending>();
+                            epilogue_bar();
+                            if (store_lead) {
+                                tma_store_3d(map_c, stg, col0, m0, b);
+                                bulk_commit();
+                            }
+                            ++n_st;
+                        } else if (row < M) {
                             if (vec_store && col0 + 32 <= N) {
-                                reinterpret_cast<uint4*>(dst)[0] = make_uint4(w[0], w[1], w[2], w[3]);
-                                reinterpret_cast<uint4*>(dst)[1] = make_uint4(w[4], w[5], w[6], w[7]);
+                                uint4* dst = reinterpret_cast<uint4*>(orow + col0);
+#pragma unroll
+                                for (int v = 0; v < 4; ++v) {
+                                    uint4 x;
+                                    x.x = pack_bf16x2(y[8 * v + 0], y[8 * v + 1]);
+                                    x.y = pack_bf16x2(y[8 * v + 2], y[8 * v + 3]);
+                                    x.z = pack_bf16x2(y[8 * v + 4], y[8 * v + 5]);
+                                    x.w = pack_bf16x2(y[8 * v + 6], y[8 * v + 7]);
+                                    dst[v] = x;
+                                }
                             } else {
 #pragma unroll
-                                for (int i = 0; i < 32; ++i)
-                                    if (col0 + i < N) dst[i] = uint8_t(w[i >> 2] >> (8 * (i & 3)));
-                            }
-                        }
-                    } else if (tma_store) {
-                        // the 128 x 32 bf16 block goes to the staging tile whose last
-                        // store is known to have read it (64-byte swizzle: 16-byte
-                        // piece j of row r at (j ^ (r / 2 mod 4)) * 16, so the 8
-                        // lanes of a store phase hit distinct banks); then one TMA
-                        // store, which clips the M / N tails of the output
-                        const uint32_t stg = stg0 + uint32_t(n_st % L::kStgBufs) * L::kStgBytes;
-#pragma unroll
-                        for (int j = 0; j < 4; ++j) {
-                            const uint32_t addr = stg + row_in_tile * 64 + ((j ^ ((row_in_tile >> 1) & 3)) << 4);
-                            asm volatile("st.shared.v4.b32 [%0], {%1, %2, %3, %4};" ::"r"(addr),
-                                         "r"(pack_bf16x2(y[8 * j + 0], y[8 * j + 1])),
-                                         "r"(pack_bf16x2(y[8 * j + 2], y[8 * j + 3])),
-                                         "r"(pack_bf16x2(y[8 * j + 4], y[8 * j + 5])),
-                                         "r"(pack_bf16x2(y[8 * j + 6], y[8 * j + 7]))
-                                         : "memory");
-                        }
-                        fence_proxy_async_smem();
-                        // the store two blocks back has read its tile, which the next
-                        // block reuses (only the newest store may still be reading);
-                        // the barrier publishes that and this block
-                        if (store_lead) bulk_wait_read<L::kStgPending>();
-                        epilogue_bar();
-                        if (store_lead) {
-                            tma_store_3d(map_c, stg, col0, m0, b);
-                            bulk_commit();
-                        }
-                        ++n_st;
-                    } else if (row < M) {
-                        if (vec_store && col0 + 32 <= N) {
-                            uint4* dst = reinterpret_cast<uint4*>(orow + col0);
-#pragma unroll
-                            for (int v = 0; v < 4; ++v) {
-                                uint4 x;
-                                x.x = pack_bf16x2(y[8 * v + 0], y[8 * v + 1]);
-                                x.y = pack_bf16x2(y[8 * v + 2], y[8 * v + 3]);
-                                x.z = pack_bf16x2(y[8 * v + 4], y[8 * v + 5]);
-                                x.w = pack_bf16x2(y[8 * v + 6], y[8 * v + 7]);
-                                dst[v] = x;
-                            }
-                        } else {
-#pragma unroll
-                            for (int i = 0; i < 32; i += 2) {
-                                const uint32_t x = pack_bf16x2(y[i], y[i + 1]);
-                                if (col0 + i < N) orow[col0 + i] = uint16_t(x & 0xFFFFu);
-                                if (col0 + i + 1 < N) orow[col0 + i + 1] = uint16_t(x >> 16);
+                                for (int i = 0; i < 32; i += 2) {
+                                    const uint32_t x = pack_bf16x2(y[i], y[i + 1]);
+                                    if (col0 + i < N) orow[col0 + i] = uint16_t(x & 0xFFFFu);
+                                    if (col0 + i + 1 < N) orow[col0 + i + 1] = uint16_t(x >> 16);
+                                }
                             }
                         }
                     }
                 }
+                tc_fence_before();
+                // release the accumulator to the MMA issuer (the pair's leader)
+                if (CTAS == 1) mbar_arrive(bar_tempty + 8 * buf);
+                else           mbar_arrive_cluster(map_to_rank(bar_tempty + 8 * buf, 0));
             }
-            tc_fence_before();
-            // release the accumulator to the MMA issuer (the pair's leader)
-            if (CTAS == 1) mbar_arrive(bar_tempty + 8 * buf);
-            else           mbar_arrive_cluster(map_to_rank(bar_tempty + 8 * buf, 0));
-        }
-        // the staging tiles must outlive the stores that read them; the global
-        // writes themselves complete with the grid (a dependent kernel's
-        // griddepcontrol.wait and stream order both see them)
-        if ((GROUP || EP || tma_store) && (EP && !SWAP ? lane == 0 : store_lead)) bulk_wait_read<0>();
-        if constexpr (OUT8) {
-            // the CTA's amax of the output: one atomicMax, then a ticket; the
-            // CTA holding the last ticket folds it into the output's ring
-            uint32_t bits = __reduce_max_sync(0xffffffffu, __float_as_uint(m_out));
-            epilogue_bar<ET>();  // the bias slots are free now
-            uint32_t* red = reinterpret_cast<uint32_t*>(s_bias);
-            if (lane == 0) red[warp - 2] = bits;
-            epilogue_bar<ET>();
-            if (etid == 0) {
-                bits = max(max(red[0], red[1]), max(red[2], red[3]));
-                for (int w = 4; w < ET / 32; ++w) bits = max(bits, red[w]);
-                fp8_ring* ring = p.out_ring;
-                if (bits != 0u) atomicMax(&ring->amax_bits, bits);
-                const uint32_t ticket = atom_add_acq_rel(&ring->ticket, 1u);
-                if (ticket == gridDim.x - 1) {
-                    volatile fp8_ring* rr = ring;
-                    float h[FP8_RING_HISTORY];
-                    const uint32_t idx = ring_read(rr, h);
-                    const float a = __uint_as_float(atomicExch(&ring->amax_bits, 0u));
-                    ring_fold(rr, h, idx, a, fmt_max(p.out_fmt));
-                    if (p.out_amax) *p.out_amax = a;
-                    rr->ticket = 0u;
-                }
+            // the staging tiles must outlive the stores that read them; the global
+            // writes themselves complete with the grid (a dependent kernel's
+            // griddepcontrol.wait and stream order both see them)
+            if ((GROUP || tma_store) && store_lead) bulk_wait_read<0>();
+            if constexpr (OUT8) {
+                out8_finish<kEpiThreads>(p, m_out, s_bias, warp, lane, etid);
             }
         }
     }
