@@ -171,29 +171,14 @@ struct Experts {
     }
 };
 
-// Tile i of one expert's mt x nt tiles: groups of 16 tile rows, M-fastest
-// inside (tile_coords, for tiles that mostly fit one group).
-__device__ __forceinline__ void expert_tile(int i, int mt, int nt, int& mb, int& nb) {
-    constexpr int kGroup = 16;
-    int first = 0;
-    if (i >= kGroup * nt) {
-        const int g = i / (kGroup * nt);
-        first = g * kGroup;
-        i -= first * nt;
-    }
-    const int rows = min(kGroup, mt - first);
-    nb = i / rows;
-    mb = first + i - nb * rows;
-}
-
 // Work unit u.
 template <int BN, int KIND, bool SWAP, int TILE>
 __device__ __forceinline__ Item item_of(Experts<TILE>& x, const ExpertParams& p, int u) {
     Item it;
-    int mb, nb;
+    int mb, nb, b;
     if constexpr (KIND == kSumTN) {
         x.find_expert(u, p.m_tiles * p.n_tiles);
-        expert_tile(u - x.u0, p.m_tiles, p.n_tiles, mb, nb);
+        tile_coords_lazy(u - x.u0, TileWalk{p.m_tiles, p.n_tiles, 16}, mb, nb, b);
         it.m0 = mb * TILE;
         it.m_end = p.M;
         it.n0 = nb * BN;
@@ -207,7 +192,7 @@ __device__ __forceinline__ Item item_of(Experts<TILE>& x, const ExpertParams& p,
             mb = u - x.u0 - nb * (x.t1 - x.t0);
             it.n0 = nb * BM;
         } else {
-            expert_tile(u - x.u0, x.t1 - x.t0, p.n_tiles, mb, nb);
+            tile_coords_lazy(u - x.u0, TileWalk{x.t1 - x.t0, p.n_tiles, 16}, mb, nb, b);
             it.n0 = nb * BN;
         }
         it.m0 = x.lo + mb * TILE;

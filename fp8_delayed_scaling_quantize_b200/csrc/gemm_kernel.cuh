@@ -336,6 +336,26 @@ __device__ __forceinline__ void tile_coords(int t, const TileWalk& w, int& mb, i
     nb = i / rows;
 }
 
+// The same without the divisions that a small problem does not need.
+__device__ __forceinline__ void tile_coords_lazy(int t, const TileWalk& w, int& mb, int& nb, int& b) {
+    b = 0;
+    const int per_batch = w.m_tiles * w.n_tiles;
+    if (t >= per_batch) {
+        b = t / per_batch;
+        t -= b * per_batch;
+    }
+    int first_m = 0;
+    const int per_group = w.group_m * w.n_tiles;
+    if (t >= per_group) {
+        const int g = t / per_group;
+        first_m = g * w.group_m;
+        t -= g * per_group;
+    }
+    const int rows = min(w.group_m, w.m_tiles - first_m);
+    nb = t / rows;
+    mb = first_m + t - nb * rows;
+}
+
 // Keeps a value's computation (a kernel-parameter read) at this point of the
 // program: the first read of each parameter is a slow constant-cache miss, so
 // the kernel issues them all together while its set-up runs.
@@ -706,7 +726,7 @@ __device__ __forceinline__ void act_epilogue(const GemmParams& p, const EpArgs<t
     };
     int mb = 0, nb = 0, b = 0;
     if (unit0 < total_units) {
-        tile_coords(unit0, walk, mb, nb, b);
+        tile_coords_lazy(unit0, walk, mb, nb, b);
         ask_bias(nb);
     }
     bool failed = false;
@@ -725,7 +745,7 @@ __device__ __forceinline__ void act_epilogue(const GemmParams& p, const EpArgs<t
 #pragma unroll
         for (int i = 0; i < kActBlocks<BN>; ++i) bias[i] = bias_next[i];
         if (u + unit_step < total_units) {
-            tile_coords(u + unit_step, walk, mb, nb, b);
+            tile_coords_lazy(u + unit_step, walk, mb, nb, b);
             ask_bias(nb);
             const int64_t row = int64_t(mb * CTAS + int(rank)) * BM + q * 32 + lane;
             if (res_vec && row < M) {
@@ -1084,6 +1104,25 @@ fp8_gemm_kernel(const __grid_constant__ CUtensorMap tm_a, const __grid_constant_
                     }
                     epilogue_bar();
                 }
+                // a swapped activation asks for its residual's first 16 rows of C and
+                // for its bias while the accumulator is still being made
+                float act_bias = 0.0f, act_res[16];
+                if constexpr (EP && SWAP) {
+                    const int col = m0 + row_in_tile;  // of C
+#pragma unroll
+                    for (int i = 0; i < 16; ++i) act_res[i] = 0.0f;
+                    if (col < M && (!csplit || split_id == 0)) {
+                        const uint16_t* res = ep.residual ? ep.residual + int64_t(b) * ep.stride_r + col : nullptr;
+#pragma unroll
+                        for (int i = 0; i < 16; ++i)
+                            if (res && nb * BN + i < N) act_res[i] = bf16_value(res[int64_t(nb * BN + i) * M]);
+                        if (bias_kind == 1)
+                            act_bias = bf16_value(__ldg(static_cast<const uint16_t*>(bias_ptr) + col));
+                        else if (bias_kind == 2)
+                            act_bias = __fdiv_rn(fp8_to_f32(__ldg(static_cast<const uint8_t*>(bias_ptr) + col), bias_fmt),
+                                                 bscale);
+                    }
+                }
                 // every lane waits, then all epilogue warps agree (and each warp
                 // reconverges) before the warp-collective TMEM loads. After a wait
                 // gave up, they all keep walking the units without waiting, so that
@@ -1165,8 +1204,8 @@ fp8_gemm_kernel(const __grid_constant__ CUtensorMap tm_a, const __grid_constant_
                 const int row = m0 + row_in_tile;
                 // swapped operands: this thread's TMEM lane is output column `row`
                 // of C (the kernel's M is C's N), its accumulator columns are C's rows
-                float bias_row = 0.0f;
-                if (SWAP && HAS_BIAS && row < M && (!EP || bias_kind != 0)) {
+                float bias_row = (EP && SWAP) ? act_bias : 0.0f;
+                if (SWAP && HAS_BIAS && !EP && row < M) {
                     if (bias_kind == 1)
                         bias_row = __uint_as_float(uint32_t(__ldg(static_cast<const uint16_t*>(bias_ptr) + row)) << 16);
                     else
@@ -1278,11 +1317,15 @@ fp8_gemm_kernel(const __grid_constant__ CUtensorMap tm_a, const __grid_constant_
                                         if (col0 + i < N) z[int64_t(col0 + i) * M] = bf16_bits(y[i]);
                                 }
                                 act_apply(ep.act, y);
-                                if (ep.residual) {
+                                if (ep.residual && c > 0) {
                                     const uint16_t* res = ep.residual + int64_t(b) * ep.stride_r + row;
 #pragma unroll
                                     for (int i = 0; i < CW; ++i)
-                                        if (col0 + i < N) y[i] += bf16_value(res[int64_t(col0 + i) * M]);
+                                        act_res[i] = col0 + i < N ? bf16_value(res[int64_t(col0 + i) * M]) : 0.0f;
+                                }
+                                if (ep.residual) {
+#pragma unroll
+                                    for (int i = 0; i < CW; ++i) y[i] += act_res[i];
                                 }
 #pragma unroll
                                 for (int i = 0; i < CW; ++i)
