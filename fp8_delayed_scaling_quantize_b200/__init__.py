@@ -107,6 +107,7 @@ def _load():
         "fp8_mm_act_out8": (I, [P, I, P, I, P, P, I, I64, I64, I64, I64, I64, I64, I64, P, P, I, I, P, I, P, P, P, P,
                                 P]),
         "fp8_mm_experts": (I, [P, I, P, I, P, P, ctypes.c_int32, I, I64, I64, I64, ctypes.c_int32, P, P, I, P, P, P]),
+        "fp8_act_grad_experts": (I, [P, P, I64, I64, ctypes.c_int32, P, I, I, P, ctypes.c_uint32, P, P, P, P, P]),
         "fp8_act_grad": (I, [P, P, I64, I64, I, I, P, ctypes.c_uint32, P, P, P, P, P]),
     }
     for name, (res, args) in sig.items():
@@ -282,6 +283,13 @@ def fp8_mm_experts(a8, fa, b8, fb, sa, sb, sb_stride, layout, M, N, K, experts, 
 def fp8_act_grad(g, z, rows, cols, act, fmt, ring, flags, out8, amax_out, scale_out, dbias, stream=None):
     return _check(lib.fp8_act_grad(_ptr(g), _ptr(z), rows, cols, act, fmt, _ptr(ring), flags, _ptr(out8),
                                    _ptr(amax_out), _ptr(scale_out), _ptr(dbias), _stream(stream)), "fp8_act_grad")
+
+
+def fp8_act_grad_experts(g, z, rows, cols, experts, offsets, act, fmt, ring, flags, out8, amax_out, scale_out, dbias,
+                         stream=None):
+    return _check(lib.fp8_act_grad_experts(_ptr(g), _ptr(z), rows, cols, experts, _ptr(offsets), act, fmt, _ptr(ring),
+                                           flags, _ptr(out8), _ptr(amax_out), _ptr(scale_out), _ptr(dbias),
+                                           _stream(stream)), "fp8_act_grad_experts")
 
 
 def fp8_mm_grouped(problems, stream=None):

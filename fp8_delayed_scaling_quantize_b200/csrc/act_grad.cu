@@ -8,8 +8,11 @@
 // each thread adds its rows, the warps meet in shared memory, and rank 0 adds
 // the other CTAs' sums through distributed shared memory. Every sum has one
 // fixed order, in fp32, with no workspace and no atomics; the cluster's amax
-// takes the same way, so the ring sees one atomic per strip. A thread covers
+// takes the same way, so the ring sees one atomic per cluster. A thread covers
 // 8 columns (16 bytes of g and of z, 8 of codes) of kRows rows at a time.
+//
+// Rows of experts (fp8_act_grad_experts): a cluster takes every `parts`-th
+// expert of its strip and finishes each one's sums before the next.
 
 #include <cuda_runtime.h>
 
@@ -41,6 +44,10 @@ struct GradArgs {
     int fmt;
     int defer;
     int ranks;  // CTAs of a cluster
+    // rows of experts: offsets[experts + 1], or NULL (one range, all rows)
+    const int32_t* offsets;
+    int experts;
+    int parts;  // clusters of a strip
 };
 
 __device__ __forceinline__ float lo_f32(uint32_t w) { return __uint_as_float(w << 16); }
@@ -93,16 +100,16 @@ __global__ void __launch_bounds__(kThreads, kPerSm) act_grad_kernel(const GradAr
     griddep_wait();
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
     const int rank = int(blockIdx.x) % a.ranks;
-    const int64_t strip = int64_t(blockIdx.x) / a.ranks;
+    const int64_t cluster = int64_t(blockIdx.x) / a.ranks;
+    const int64_t strip = cluster / a.parts;
+    const int part0 = int(cluster - strip * a.parts);
     const int64_t piece = strip * kTpr + threadIdx.x % kTpr;  // this thread's 8 columns
     const bool in = piece < a.pitch;
     const int64_t step = int64_t(a.ranks) * kBlockRows;  // rows between two of this thread
-    const int64_t row = int64_t(rank) * kBlockRows + threadIdx.x / kTpr;
-    int n = in && row < a.rows ? int((a.rows - row + step - 1) / step) : 0;  // rows left
-    int64_t at = row * a.pitch + piece;
     const int64_t stride = step * a.pitch;
-    const uint4* pg = a.g + at;  // the row to load next
-    const uint4* pz = a.z + at;
+    const int64_t first = int64_t(rank) * kBlockRows + threadIdx.x / kTpr;  // this thread's first row of a range
+    const uint4* pg = nullptr;  // the row to load next
+    const uint4* pz = nullptr;
     uint4 g[kRows], z[kRows];
     auto load = [&](int u) {
         g[u] = __ldg(pg);
@@ -112,114 +119,131 @@ __global__ void __launch_bounds__(kThreads, kPerSm) act_grad_kernel(const GradAr
             pz += stride;
         }
     };
+    float s = 0.0f, m = 0.0f;
+    for (int e = part0; e < a.experts; e += a.parts) {
+        int64_t lo = 0, hi = a.rows;
+        if (a.offsets) {  // limited to the rows there are
+            lo = min(max(int64_t(__ldg(a.offsets + e)), int64_t(0)), a.rows);
+            hi = min(max(int64_t(__ldg(a.offsets + e + 1)), lo), a.rows);
+        }
+        const int64_t row = lo + first;
+        int n = in && row < hi ? int((hi - row + step - 1) / step) : 0;  // rows left
+        const int64_t at = row * a.pitch + piece;
+        pg = a.g + at;
+        pz = a.z + at;
 #pragma unroll
-    for (int u = 0; u < kRows; ++u)
-        if (u < n) load(u);  // before the scale is known: the loads do not need it
-    if (threadIdx.x == 0) {
-        s_scale = *reinterpret_cast<volatile float*>(&a.ring->scale);
-        if (blockIdx.x == 0) *a.scale_out = s_scale;
-    }
-    __syncthreads();
-    const float s = s_scale;
-    float m = 0.0f;
-    F2 sum[4] = {0, 0, 0, 0};
-    uint2* out = a.out8 + at;
-    while (n > 0) {
+        for (int u = 0; u < kRows; ++u)
+            if (u < n) load(u);  // before the scale is known: the loads do not need it
+        if (e == part0) {
+            if (threadIdx.x == 0) {
+                s_scale = *reinterpret_cast<volatile float*>(&a.ring->scale);
+                if (blockIdx.x == 0) *a.scale_out = s_scale;
+            }
+            __syncthreads();
+            s = s_scale;
+        }
+        F2 sum[4] = {0, 0, 0, 0};
+        uint2* out = a.out8 + at;
+        while (n > 0) {
 #pragma unroll
-        for (int u = 0; u < kRows; ++u) {
-            if (u < n) {
-                const uint32_t gw[4] = {g[u].x, g[u].y, g[u].z, g[u].w};
-                const uint32_t zw[4] = {z[u].x, z[u].y, z[u].z, z[u].w};
-                F2 d[4];
+            for (int u = 0; u < kRows; ++u) {
+                if (u < n) {
+                    const uint32_t gw[4] = {g[u].x, g[u].y, g[u].z, g[u].w};
+                    const uint32_t zw[4] = {z[u].x, z[u].y, z[u].z, z[u].w};
+                    F2 d[4];
 #pragma unroll
-                for (int i = 0; i < 4; ++i) {
-                    d[i] = f2(lo_f32(gw[i]), hi_f32(gw[i]));
-                    if (ACT != FP8_ACT_NONE) d[i] = mul2(d[i], act_slope<ACT>(zw[i]));
+                    for (int i = 0; i < 4; ++i) {
+                        d[i] = f2(lo_f32(gw[i]), hi_f32(gw[i]));
+                        if (ACT != FP8_ACT_NONE) d[i] = mul2(d[i], act_slope<ACT>(zw[i]));
+                    }
+                    if (u + kRows < n) load(u);  // the registers are free: the row kRows further on
+#pragma unroll
+                    for (int i = 0; i < 4; ++i) {
+                        m = max_abs(m, d[i]);
+                        sum[i] = add2(sum[i], d[i]);
+                    }
+                    *out = a.fmt == FP8_E4M3 ? codes8<FP8_E4M3>(d, s) : codes8<FP8_E5M2>(d, s);
+                    out += stride;
                 }
-                if (u + kRows < n) load(u);  // the registers are free: the row kRows further on
+            }
+            n -= kRows;
+        }
+        if (!a.dbias) continue;
+        // the block's column sums, then the cluster's: rank 0 adds them in rank order
 #pragma unroll
-                for (int i = 0; i < 4; ++i) {
-                    m = max_abs(m, d[i]);
-                    sum[i] = add2(sum[i], d[i]);
-                }
-                *out = a.fmt == FP8_E4M3 ? codes8<FP8_E4M3>(d, s) : codes8<FP8_E5M2>(d, s);
-                out += stride;
+        for (int i = 0; i < 4; ++i) {
+            float v0, v1;
+            split(sum[i], v0, v1);
+#pragma unroll
+            for (int o = kTpr; o < 32; o <<= 1) {
+                v0 += __shfl_xor_sync(0xffffffffu, v0, o);
+                v1 += __shfl_xor_sync(0xffffffffu, v1, o);
+            }
+            if (lane < kTpr) {
+                part[warp][lane * 8 + 2 * i] = v0;
+                part[warp][lane * 8 + 2 * i + 1] = v1;
             }
         }
-        n -= kRows;
+        __syncthreads();
+        if (threadIdx.x < W) {
+            float v = 0.0f;
+#pragma unroll
+            for (int w = 0; w < kWarps; ++w) v += part[w][threadIdx.x];
+            colsum[threadIdx.x] = v;
+        }
+        if (a.ranks > 1) cluster_sync();
+        if (rank == 0 && threadIdx.x < W) {
+            float v = colsum[threadIdx.x];
+            const uint32_t mine = smem_addr(&colsum[threadIdx.x]);
+            for (int r = 1; r < a.ranks; ++r) v += ld_cluster_f32(map_to_rank(mine, uint32_t(r)));
+            const int64_t c = strip * W + threadIdx.x;
+            if (c < a.pitch * 8) {
+                uint16_t h;
+                asm("cvt.rn.bf16.f32 %0, %1;" : "=h"(h) : "f"(v));
+                a.dbias[int64_t(e) * a.pitch * 8 + c] = h;
+            }
+        }
+        // rank 0 has read every sum before they change, and the block its own parts
+        if (a.ranks > 1) cluster_sync();
+        else             __syncthreads();
     }
     griddep_launch();
-    // the block's sums and amax
-#pragma unroll
-    for (int i = 0; i < 4; ++i) {
-        float v0, v1;
-        split(sum[i], v0, v1);
-#pragma unroll
-        for (int o = kTpr; o < 32; o <<= 1) {
-            v0 += __shfl_xor_sync(0xffffffffu, v0, o);
-            v1 += __shfl_xor_sync(0xffffffffu, v1, o);
-        }
-        if (lane < kTpr) {
-            part[warp][lane * 8 + 2 * i] = v0;
-            part[warp][lane * 8 + 2 * i + 1] = v1;
-        }
-    }
     const uint32_t bits = __reduce_max_sync(0xffffffffu, __float_as_uint(m));
     if (lane == 0) wmax[warp] = bits;
     __syncthreads();
-    if (threadIdx.x < W) {
-        float v = 0.0f;
-#pragma unroll
-        for (int w = 0; w < kWarps; ++w) v += part[w][threadIdx.x];
-        colsum[threadIdx.x] = v;
-    }
     if (threadIdx.x == 0) {
         uint32_t b = wmax[0];
 #pragma unroll
         for (int w = 1; w < kWarps; ++w) b = max(b, wmax[w]);
         bmax = __uint_as_float(b);
     }
-    // the cluster's: rank 0 adds them in rank order
-    cluster_sync();
-    if (rank == 0) {
-        if (threadIdx.x < W && a.dbias) {
-            float v = colsum[threadIdx.x];
-            const uint32_t at = smem_addr(&colsum[threadIdx.x]);
-            for (int r = 1; r < a.ranks; ++r) v += ld_cluster_f32(map_to_rank(at, uint32_t(r)));
-            const int64_t c = strip * W + threadIdx.x;
-            if (c < a.pitch * 8) {
-                uint16_t h;
-                asm("cvt.rn.bf16.f32 %0, %1;" : "=h"(h) : "f"(v));
-                a.dbias[c] = h;
+    if (a.ranks > 1) cluster_sync();
+    if (rank == 0 && threadIdx.x == 0) {
+        float v = bmax;
+        for (int r = 1; r < a.ranks; ++r) v = fmaxf(v, ld_cluster_f32(map_to_rank(smem_addr(&bmax), uint32_t(r))));
+        fp8_ring* ring = a.ring;
+        if (v != 0.0f) atomicMax(&ring->amax_bits, __float_as_uint(v));
+        const uint32_t ticket = atom_add_acq_rel(&ring->ticket, 1u);
+        if (ticket == gridDim.x / a.ranks - 1) {
+            volatile fp8_ring* rr = ring;
+            if (a.defer) {
+                if (a.amax_out) *a.amax_out = __uint_as_float(*reinterpret_cast<volatile uint32_t*>(&ring->amax_bits));
+            } else {
+                float h[FP8_RING_HISTORY];
+                const uint32_t idx = ring_read(rr, h);
+                const float top = __uint_as_float(atomicExch(&ring->amax_bits, 0u));
+                ring_fold(rr, h, idx, top, fmt_max(a.fmt));
+                if (a.amax_out) *a.amax_out = top;
             }
-        }
-        if (threadIdx.x == 0) {
-            float v = bmax;
-            for (int r = 1; r < a.ranks; ++r) v = fmaxf(v, ld_cluster_f32(map_to_rank(smem_addr(&bmax), uint32_t(r))));
-            fp8_ring* ring = a.ring;
-            if (v != 0.0f) atomicMax(&ring->amax_bits, __float_as_uint(v));
-            const uint32_t ticket = atom_add_acq_rel(&ring->ticket, 1u);
-            if (ticket == gridDim.x / a.ranks - 1) {
-                volatile fp8_ring* rr = ring;
-                if (a.defer) {
-                    if (a.amax_out) *a.amax_out = __uint_as_float(*reinterpret_cast<volatile uint32_t*>(&ring->amax_bits));
-                } else {
-                    float h[FP8_RING_HISTORY];
-                    const uint32_t idx = ring_read(rr, h);
-                    const float top = __uint_as_float(atomicExch(&ring->amax_bits, 0u));
-                    ring_fold(rr, h, idx, top, fmt_max(a.fmt));
-                    if (a.amax_out) *a.amax_out = top;
-                }
-                rr->ticket = 0u;
-            }
+            rr->ticket = 0u;
         }
     }
-    cluster_sync();  // no CTA leaves while rank 0 may still read its shared memory
+    if (a.ranks > 1) cluster_sync();  // no CTA leaves while rank 0 may still read its shared memory
 }
 
 template <int W>
 fp8_status launch_width(const GradArgs& a, int act, int64_t strips, cudaStream_t st) {
-    const dim3 grid(unsigned(strips * a.ranks));
+    const dim3 grid(unsigned(strips * a.parts * a.ranks));
     switch (act) {
         case FP8_ACT_NONE: return launch_pdl(act_grad_kernel<FP8_ACT_NONE, W>, grid, kThreads, 0, st, a.ranks, a);
         case FP8_ACT_RELU: return launch_pdl(act_grad_kernel<FP8_ACT_RELU, W>, grid, kThreads, 0, st, a.ranks, a);
@@ -235,10 +259,13 @@ fp8_status launch_width(const GradArgs& a, int act, int64_t strips, cudaStream_t
 
 using namespace fp8lite;
 
-extern "C" fp8_status fp8_act_grad(const void* g, const void* z, int64_t rows, int64_t cols, fp8_act act, fp8_fmt fmt,
-                                   fp8_ring* ring, uint32_t flags, uint8_t* out8, float* amax_out, float* scale_out,
-                                   void* dbias, void* stream) {
-    if (!valid_act(int(act)) || !valid_fmt(int(fmt))) return FP8_ERR_INVALID_ARG;
+namespace fp8lite {
+namespace {
+
+fp8_status act_grad_impl(const void* g, const void* z, int64_t rows, int64_t cols, int experts, const int32_t* offsets,
+                         int act, int fmt, fp8_ring* ring, uint32_t flags, uint8_t* out8, float* amax_out,
+                         float* scale_out, void* dbias, void* stream) {
+    if (!valid_act(act) || !valid_fmt(fmt)) return FP8_ERR_INVALID_ARG;
     if (flags != 0 && flags != FP8_QUANTIZE_DEFER_FOLD) return FP8_ERR_INVALID_ARG;
     if (rows < 0 || cols < 1 || cols >= (int64_t(1) << 31) || rows >= (int64_t(1) << 31) ||
         rows >= (int64_t(1) << 40) / cols)
@@ -247,7 +274,8 @@ extern "C" fp8_status fp8_act_grad(const void* g, const void* z, int64_t rows, i
     if (rows > 0 && (!g || !out8 || (act != FP8_ACT_NONE && !z))) return FP8_ERR_INVALID_ARG;
     if (cols % 8 != 0) return FP8_ERR_ALIGNMENT;
     if (!aligned(g, 16) || !aligned(z, 16) || !aligned(out8, 16) || !aligned(dbias, 2)) return FP8_ERR_ALIGNMENT;
-    if (!aligned(ring, 4) || !aligned(amax_out, 4) || !aligned(scale_out, 4)) return FP8_ERR_ALIGNMENT;
+    if (!aligned(ring, 4) || !aligned(amax_out, 4) || !aligned(scale_out, 4) || !aligned(offsets, 4))
+        return FP8_ERR_ALIGNMENT;
     GradArgs a = {};
     a.g = static_cast<const uint4*>(g);
     a.z = static_cast<const uint4*>(z);
@@ -258,18 +286,45 @@ extern "C" fp8_status fp8_act_grad(const void* g, const void* z, int64_t rows, i
     a.amax_out = amax_out;
     a.scale_out = scale_out;
     a.dbias = static_cast<uint16_t*>(dbias);
-    a.fmt = int(fmt);
+    a.fmt = fmt;
     a.defer = flags == FP8_QUANTIZE_DEFER_FOLD;
+    a.offsets = offsets;
+    a.experts = experts;
     // Strips of 64 columns (a row piece is one 128-byte line) unless they are
-    // too few to give every SM two CTAs; as many CTAs to a strip as stay
-    // resident together and have rows.
+    // too few to give every SM two CTAs. Then as many CTAs as stay resident
+    // together: experts first (their sums need no exchange), and to an expert
+    // as many CTAs of a cluster as its mean rows can feed.
     const auto strips = [&](int w) { return (cols + w - 1) / w; };
-    const int w = strips(64) * kMaxRanks >= 2 * 148 ? 64 : strips(32) * kMaxRanks >= 2 * 148 ? 32 : 16;
-    const int64_t blocks = (rows + kThreads / (w / 8) - 1) / (kThreads / (w / 8));
+    const int64_t slots = kPerSm * 148;
+    const int w = strips(64) * experts * kMaxRanks >= 2 * 148 ? 64 : strips(32) * experts * kMaxRanks >= 2 * 148 ? 32 : 16;
+    const int64_t n = strips(w);
+    a.parts = int(n * experts <= slots ? experts : slots / n < 1 ? 1 : slots / n);
+    const int64_t block_rows = kThreads / (w / 8);
+    const int64_t blocks = (rows / experts + block_rows - 1) / block_rows;
     a.ranks = 1;
-    while (a.ranks < kMaxRanks && a.ranks < blocks && strips(w) * a.ranks * 2 <= kPerSm * 148) a.ranks *= 2;
+    while (a.ranks < kMaxRanks && a.ranks < blocks && n * a.parts * a.ranks * 2 <= slots) a.ranks *= 2;
     cudaStream_t st = as_stream(stream);
-    if (w == 64) return launch_width<64>(a, int(act), strips(64), st);
-    if (w == 32) return launch_width<32>(a, int(act), strips(32), st);
-    return launch_width<16>(a, int(act), strips(16), st);
+    if (w == 64) return launch_width<64>(a, act, n, st);
+    if (w == 32) return launch_width<32>(a, act, n, st);
+    return launch_width<16>(a, act, n, st);
+}
+
+}  // namespace
+}  // namespace fp8lite
+
+extern "C" fp8_status fp8_act_grad(const void* g, const void* z, int64_t rows, int64_t cols, fp8_act act, fp8_fmt fmt,
+                                   fp8_ring* ring, uint32_t flags, uint8_t* out8, float* amax_out, float* scale_out,
+                                   void* dbias, void* stream) {
+    return act_grad_impl(g, z, rows, cols, 1, nullptr, int(act), int(fmt), ring, flags, out8, amax_out, scale_out, dbias,
+                         stream);
+}
+
+extern "C" fp8_status fp8_act_grad_experts(const void* g, const void* z, int64_t rows, int64_t cols, int32_t experts,
+                                           const int32_t* offsets, fp8_act act, fp8_fmt fmt, fp8_ring* ring,
+                                           uint32_t flags, uint8_t* out8, float* amax_out, float* scale_out,
+                                           void* dbias, void* stream) {
+    if (experts < 1 || !offsets) return FP8_ERR_INVALID_ARG;
+    if (experts > FP8_MM_MAX_EXPERTS) return FP8_ERR_UNSUPPORTED;
+    return act_grad_impl(g, z, rows, cols, experts, offsets, int(act), int(fmt), ring, flags, out8, amax_out, scale_out,
+                         dbias, stream);
 }

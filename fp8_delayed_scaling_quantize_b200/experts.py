@@ -1,0 +1,106 @@
+"""FP8 training linear layer of a mixture of experts (torch.autograd).
+
+The rows of the input are sorted by expert: rows [offsets[e], offsets[e+1])
+belong to expert e. The offsets stay on the device; nothing is synchronised,
+so a layer whose routing changes from step to step can be captured into a CUDA
+graph. Each of the layer's products is one launch over all experts
+(fp8_mm_experts: forward NT with bias and activation, input gradient NN,
+weight gradient TN), and the gradient through the activation is quantized with
+the experts' bias gradients in one pass (fp8_act_grad_experts).
+
+Scaling is delayed and per tensor: one ring each for the input, the weights of
+all experts and the gradient, kept in `fp8_rings` with the state_dict.
+"""
+
+import torch
+
+from . import (FP8_ACT_NONE, FP8_E4M3, FP8_E5M2, FP8_NN, FP8_NT, FP8_TN, fp8_act_grad_experts, fp8_mm_experts,
+               fp8_ring_init)
+from .linear import _RING_WORDS, _act_code, _quantize_many, _rows_of
+
+
+class Fp8ExpertsFunction(torch.autograd.Function):
+    """y[r] = act(x[r] W[e]^T + b[e]) for the rows r of expert e; rows of no
+    expert give zeros and get zero gradients."""
+
+    @staticmethod
+    def forward(ctx, x, offsets, weight, bias, rings, act):
+        E, N, K = weight.shape
+        x2 = _rows_of(x, K, "input")
+        if x.dim() != 2:
+            raise ValueError("experts take token-sorted rows [T, features]")
+        if offsets.dtype != torch.int32 or offsets.shape != (E + 1,) or offsets.device != x.device:
+            raise ValueError(f"offsets must be int32 [{E + 1}] on the input's device")
+        T, dev = x2.shape[0], x.device
+        offsets = offsets.contiguous()
+        (x8, sx), (w8, sw) = _quantize_many([(x2, FP8_E4M3, rings[0]), (weight.contiguous(), FP8_E4M3, rings[1])], dev)
+        y = torch.zeros(T, N, dtype=torch.bfloat16, device=dev)  # rows of no expert
+        z = None
+        if act != FP8_ACT_NONE and (ctx.needs_input_grad[0] or any(ctx.needs_input_grad[2:4])):
+            z = torch.empty(T, N, dtype=torch.bfloat16, device=dev)
+        b = bias.contiguous() if bias is not None else None
+        fp8_mm_experts(x8, FP8_E4M3, w8, FP8_E4M3, sx, sw, 0, FP8_NT, T, N, K, E, offsets, b, act, z, y)
+        ctx.save_for_backward(x8, w8, sx, sw, rings, offsets, z)
+        ctx.dims, ctx.act, ctx.has_bias = (T, N, K, E), act, bias is not None
+        return y
+
+    @staticmethod
+    def backward(ctx, gy):
+        x8, w8, sx, sw, rings, offsets, z = ctx.saved_tensors
+        T, N, K, E = ctx.dims
+        need_x, need_w, need_b = ctx.needs_input_grad[0], ctx.needs_input_grad[2], ctx.needs_input_grad[3]
+        dx = dw = db = None
+        dev = gy.device
+        g2 = gy.to(torch.bfloat16).contiguous()
+        g8 = torch.empty(T * N, dtype=torch.uint8, device=dev)
+        stats = torch.empty(2, dtype=torch.float32, device=dev)
+        if need_b and ctx.has_bias:
+            db = torch.empty(E, N, dtype=torch.bfloat16, device=dev)
+        fp8_act_grad_experts(g2, z, T, N, E, offsets, ctx.act, FP8_E5M2, rings[2], 0, g8, stats[0:1], stats[1:2], db)
+        sg = stats[1:2]
+        if need_x:
+            dx = torch.zeros(T, K, dtype=torch.bfloat16, device=dev)
+            fp8_mm_experts(g8, FP8_E5M2, w8, FP8_E4M3, sg, sw, 0, FP8_NN, T, K, N, E, offsets, None, FP8_ACT_NONE, None, dx)
+        if need_w:
+            dw = torch.empty(E, N, K, dtype=torch.bfloat16, device=dev)
+            fp8_mm_experts(g8, FP8_E5M2, x8, FP8_E4M3, sg, sx, 0, FP8_TN, N, K, T, E, offsets, None, FP8_ACT_NONE, None, dw)
+        return dx, None, dw, db, None, None
+
+
+class Fp8Experts(torch.nn.Module):
+    """The linears of `experts` experts (bf16 parameters, FP8 compute).
+
+    in_features and out_features must be multiples of 16. forward(x, offsets):
+    x bf16 [T, in_features] sorted by expert, offsets int32 [experts + 1] on the
+    same device. activation as Fp8Linear's. Rows of no expert give zeros; their
+    input values still count for the input's scale.
+    """
+
+    def __init__(self, experts, in_features, out_features, bias=True, device=None, activation=None):
+        super().__init__()
+        if in_features % 16 or out_features % 16:
+            raise ValueError("Fp8Experts needs in_features and out_features divisible by 16")
+        self.experts, self.in_features, self.out_features = experts, in_features, out_features
+        self.activation = activation
+        self._act = _act_code(activation)
+        kw = {"device": device, "dtype": torch.bfloat16}
+        self.weight = torch.nn.Parameter(torch.empty(experts, out_features, in_features, **kw))
+        self.bias = torch.nn.Parameter(torch.zeros(experts, out_features, **kw)) if bias else None
+        self.register_buffer("fp8_rings", torch.zeros(3, _RING_WORDS, dtype=torch.int32, device=device))
+        self._rings_ready = False
+        torch.nn.init.normal_(self.weight, std=in_features ** -0.5)
+
+    def reset_scaling(self):
+        """Reset the three rings (scale 1, empty history)."""
+        for i in range(3):
+            fp8_ring_init(self.fp8_rings[i], 1.0)
+        self._rings_ready = True
+
+    def _load_from_state_dict(self, *args, **kwargs):
+        super()._load_from_state_dict(*args, **kwargs)
+        self._rings_ready = True  # restored rings are used as they are
+
+    def forward(self, x, offsets):
+        if not self._rings_ready:
+            self.reset_scaling()
+        return Fp8ExpertsFunction.apply(x, offsets, self.weight, self.bias, self.fp8_rings, self._act)

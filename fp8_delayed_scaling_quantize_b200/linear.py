@@ -20,14 +20,45 @@ buffers and the stream. The forward saves the FP8 codes of x and W (one byte
 per element) rather than the bf16 tensors. The rings are a registered buffer
 (`fp8_rings`, three 80-byte rings), so they travel with the module's
 state_dict for checkpoint and resume.
+
+With an activation or a residual the same layer runs through the GEMM's
+activation epilogue, y = act(x W^T + b) + residual in one launch, and its
+backward pass quantizes the gradient through the activation, with the bias
+gradient, in one pass (`Fp8LinearActFunction`). `Fp8MLP` is two such linears
+whose hidden activation leaves the first product as FP8 codes: no bf16 hidden
+tensor and no quantize pass of it in the forward.
+
+The layers can be captured into a CUDA graph, forward and backward. As for any
+torch module, no eager autograd graph of the same parameters may live at that
+time (an output that was kept, say): its leaves are bound to the eager stream,
+and torch would make that stream wait for the capture.
 """
 
 import torch
 
-from . import (FP8_E4M3, FP8_E5M2, FP8_NN, FP8_NT, FP8_RING_BYTES, FP8_TN, fp8_bias_grad, fp8_mm, fp8_mm_grouped,
-               fp8_quantize, fp8_quantize_many, fp8_ring_init)
+from . import (FP8_ACT_GELU, FP8_ACT_GELU_TANH, FP8_ACT_NONE, FP8_ACT_RELU, FP8_ACT_SILU, FP8_E4M3, FP8_E5M2, FP8_NN,
+               FP8_NT, FP8_RING_BYTES, FP8_TN, fp8_act_grad, fp8_bias_grad, fp8_mm, fp8_mm_act, fp8_mm_act_out8,
+               fp8_mm_grouped, fp8_quantize, fp8_quantize_many, fp8_ring_init)
 
 _RING_WORDS = FP8_RING_BYTES // 4
+
+ACTIVATIONS = {None: FP8_ACT_NONE, "relu": FP8_ACT_RELU, "gelu": FP8_ACT_GELU, "gelu_tanh": FP8_ACT_GELU_TANH,
+               "silu": FP8_ACT_SILU}
+
+
+def _act_code(activation):
+    if activation not in ACTIVATIONS:
+        raise ValueError(f"activation {activation!r} is none of {sorted(a for a in ACTIVATIONS if a)}")
+    return ACTIVATIONS[activation]
+
+
+def _rows_of(x, features, what):
+    """x as contiguous rows [T, features]."""
+    if x.shape[-1] != features:
+        raise ValueError(f"{what} features {x.shape[-1]} != {features}")
+    if x.dtype != torch.bfloat16:
+        raise TypeError(f"{what} must be bf16")
+    return x.reshape(-1, features).contiguous()
 
 
 def _quantize(t, n, fmt, ring):
@@ -99,15 +130,101 @@ class Fp8LinearFunction(torch.autograd.Function):
         return dx, dw, db, None
 
 
+def _quantize_many(jobs, device):
+    """Delayed quantizes in one launch: jobs (tensor, fmt, ring) -> [(codes, scale)]."""
+    stats = torch.empty(2 * len(jobs), dtype=torch.float32, device=device)
+    out = [torch.empty(t.numel(), dtype=torch.uint8, device=device) for t, _, _ in jobs]
+    fp8_quantize_many([(t if t.numel() else None, t.numel(), fmt, ring, q if t.numel() else None, stats[i:i + 1],
+                        stats[len(jobs) + i:len(jobs) + i + 1])
+                       for i, ((t, fmt, ring), q) in enumerate(zip(jobs, out))])
+    return [(q, stats[len(jobs) + i:len(jobs) + i + 1]) for i, q in enumerate(out)]
+
+
+def _grad_codes(g2, z, act, ring, need_bias):
+    """E5M2 codes of g act'(z), their scale and the bias gradient, in one pass."""
+    T, N = g2.shape
+    g8 = torch.empty(T * N, dtype=torch.uint8, device=g2.device)
+    stats = torch.empty(2, dtype=torch.float32, device=g2.device)
+    db = torch.empty(N, dtype=torch.bfloat16, device=g2.device) if need_bias else None
+    fp8_act_grad(g2, z, T, N, act, FP8_E5M2, ring, 0, g8, stats[0:1], stats[1:2], db)
+    return g8, stats[1:2], db
+
+
+def _dx_dw(g8, sg, w8, sw, x8, sx, T, N, K, need_x, need_w):
+    """dX = g W and dW = g^T x from the codes; both in one grouped launch."""
+    dx = torch.empty(T, K, dtype=torch.bfloat16, device=g8.device) if need_x else None
+    dw = torch.empty(N, K, dtype=torch.bfloat16, device=g8.device) if need_w else None
+    probs = []
+    if need_x:
+        probs.append((g8, FP8_E5M2, w8, FP8_E4M3, sg, sw, FP8_NN, T, K, N, None, None, 0, dx))
+    if need_w:
+        probs.append((g8, FP8_E5M2, x8, FP8_E4M3, sg, sx, FP8_TN, N, K, T, None, None, 0, dw))
+    if probs:
+        fp8_mm_grouped(probs)
+    return dx, dw
+
+
+class Fp8LinearActFunction(torch.autograd.Function):
+    """y = act(x W^T + b) + residual with FP8 operands and delayed scaling."""
+
+    @staticmethod
+    def forward(ctx, x, weight, bias, rings, act, residual):
+        N, K = weight.shape
+        x2 = _rows_of(x, K, "input")
+        T = x2.shape[0]
+        if weight.dtype != torch.bfloat16:
+            raise TypeError("Fp8Linear takes bf16 inputs and weights")
+        r2 = None
+        if residual is not None:
+            if residual.shape != (*x.shape[:-1], N):
+                raise ValueError(f"residual shape {tuple(residual.shape)} != {(*x.shape[:-1], N)}")
+            r2 = _rows_of(residual, N, "residual")
+        dev = x.device
+        (x8, sx), (w8, sw) = _quantize_many([(x2, FP8_E4M3, rings[0]), (weight.contiguous(), FP8_E4M3, rings[1])], dev)
+        y = torch.empty(T, N, dtype=torch.bfloat16, device=dev)
+        z = None
+        if act != FP8_ACT_NONE and any(ctx.needs_input_grad[:3]):
+            z = torch.empty(T, N, dtype=torch.bfloat16, device=dev)
+        b = bias.contiguous() if bias is not None else None
+        if T:
+            fp8_mm_act(x8, FP8_E4M3, w8, FP8_E4M3, sx, sw, FP8_NT, T, N, K, 1, 0, 0, 0, b, None, 0, act, r2, 0, z, y)
+        ctx.save_for_backward(x8, w8, sx, sw, rings, z)
+        ctx.dims, ctx.act, ctx.x_shape, ctx.has_bias = (T, N, K), act, x.shape, bias is not None
+        return y.reshape(*x.shape[:-1], N)
+
+    @staticmethod
+    def backward(ctx, gy):
+        x8, w8, sx, sw, rings, z = ctx.saved_tensors
+        T, N, K = ctx.dims
+        need_x, need_w, need_b = ctx.needs_input_grad[:3]
+        need_b = need_b and ctx.has_bias
+        dx = dw = db = None
+        if need_x or need_w or need_b:
+            g2 = gy.reshape(-1, N).to(torch.bfloat16).contiguous()
+            g8, sg, db = _grad_codes(g2, z, ctx.act, rings[2], need_b)
+            if T:
+                dx, dw = _dx_dw(g8, sg, w8, sw, x8, sx, T, N, K, need_x, need_w)
+            else:
+                dx = torch.empty(T, K, dtype=torch.bfloat16, device=gy.device) if need_x else None
+                dw = torch.zeros(N, K, dtype=torch.bfloat16, device=gy.device) if need_w else None
+            if need_x:
+                dx = dx.reshape(ctx.x_shape)
+        return dx, dw, db, None, None, gy if ctx.needs_input_grad[5] else None
+
+
 class Fp8Linear(torch.nn.Module):
     """Drop-in training linear layer (bf16 parameters, FP8 compute).
 
     in_features and out_features must be multiples of 16 (the GEMMs read
-    every operand through 16-byte-aligned rows).
+    every operand through 16-byte-aligned rows). activation: None, "relu",
+    "gelu", "gelu_tanh" or "silu", applied to the output in the GEMM's
+    epilogue; forward(x, residual) adds a bf16 residual after it.
     """
 
-    def __init__(self, in_features, out_features, bias=True, device=None):
+    def __init__(self, in_features, out_features, bias=True, device=None, activation=None):
         super().__init__()
+        self.activation = activation
+        self._act = _act_code(activation)
         if in_features % 16 or out_features % 16:
             raise ValueError("Fp8Linear needs in_features and out_features divisible by 16")
         self.in_features, self.out_features = in_features, out_features
@@ -128,7 +245,109 @@ class Fp8Linear(torch.nn.Module):
         super()._load_from_state_dict(*args, **kwargs)
         self._rings_ready = True  # restored rings are used as they are
 
-    def forward(self, x):
+    def forward(self, x, residual=None):
         if not self._rings_ready:
             self.reset_scaling()
-        return Fp8LinearFunction.apply(x, self.weight, self.bias, self.fp8_rings)
+        if self._act == FP8_ACT_NONE and residual is None:
+            return Fp8LinearFunction.apply(x, self.weight, self.bias, self.fp8_rings)
+        return Fp8LinearActFunction.apply(x, self.weight, self.bias, self.fp8_rings, self._act, residual)
+
+
+class Fp8MLPFunction(torch.autograd.Function):
+    """y = act(x W1^T + b1) W2^T + b2 + residual. The hidden activation goes
+    from the first product to the second as E4M3 codes under its own ring; the
+    backward pass keeps its input z in bf16. Rings: x, W1, hidden, W2, the
+    gradients of the output and of z."""
+
+    @staticmethod
+    def forward(ctx, x, w1, b1, w2, b2, rings, act, residual):
+        H, D = w1.shape
+        N = w2.shape[0]
+        x2 = _rows_of(x, D, "input")
+        T, dev = x2.shape[0], x.device
+        r2 = None
+        if residual is not None:
+            if residual.shape != (*x.shape[:-1], N):
+                raise ValueError(f"residual shape {tuple(residual.shape)} != {(*x.shape[:-1], N)}")
+            r2 = _rows_of(residual, N, "residual")
+        b1, b2 = (b.contiguous() if b is not None else None for b in (b1, b2))
+        (x8, sx), (w18, sw1), (w28, sw2) = _quantize_many(
+            [(x2, FP8_E4M3, rings[0]), (w1.contiguous(), FP8_E4M3, rings[1]), (w2.contiguous(), FP8_E4M3, rings[3])], dev)
+        z = torch.empty(T, H, dtype=torch.bfloat16, device=dev) if any(ctx.needs_input_grad[:5]) else None
+        h8 = torch.empty(T * H, dtype=torch.uint8, device=dev)
+        stats = torch.empty(2, dtype=torch.float32, device=dev)
+        sh = stats[1:2]
+        y = torch.empty(T, N, dtype=torch.bfloat16, device=dev)
+        if T:
+            fp8_mm_act_out8(x8, FP8_E4M3, w18, FP8_E4M3, sx, sw1, FP8_NT, T, H, D, 1, 0, 0, 0, b1, None, 0, act, z,
+                            FP8_E4M3, rings[2], h8, stats[0:1], sh)
+            fp8_mm_act(h8, FP8_E4M3, w28, FP8_E4M3, sh, sw2, FP8_NT, T, N, H, 1, 0, 0, 0, b2, None, 0, FP8_ACT_NONE, r2,
+                       0, None, y)
+        ctx.save_for_backward(x8, w18, h8, w28, sx, sw1, sh, sw2, rings, z)
+        ctx.dims, ctx.act, ctx.x_shape = (T, D, H, N), act, x.shape
+        return y.reshape(*x.shape[:-1], N)
+
+    @staticmethod
+    def backward(ctx, gy):
+        x8, w18, h8, w28, sx, sw1, sh, sw2, rings, z = ctx.saved_tensors
+        T, D, H, N = ctx.dims
+        need_x, need_w1, need_b1, need_w2, need_b2 = ctx.needs_input_grad[:5]
+        dx = dw1 = db1 = dw2 = db2 = None
+        inner = need_x or need_w1 or need_b1
+        if T and (inner or need_w2 or need_b2):
+            g2 = gy.reshape(-1, N).to(torch.bfloat16).contiguous()
+            g8, sg, db2 = _grad_codes(g2, None, FP8_ACT_NONE, rings[4], need_b2)
+            dh, dw2 = _dx_dw(g8, sg, w28, sw2, h8, sh, T, N, H, inner, need_w2)
+            if inner:
+                z8, sz, db1 = _grad_codes(dh, z, ctx.act, rings[5], need_b1)
+                dx, dw1 = _dx_dw(z8, sz, w18, sw1, x8, sx, T, H, D, need_x, need_w1)
+            if need_x:
+                dx = dx.reshape(ctx.x_shape)
+        elif not T:
+            zero = lambda *s: torch.zeros(*s, dtype=torch.bfloat16, device=gy.device)  # noqa: E731
+            dx = zero(*ctx.x_shape) if need_x else None
+            dw1, db1 = zero(H, D) if need_w1 else None, zero(H) if need_b1 else None
+            dw2, db2 = zero(N, H) if need_w2 else None, zero(N) if need_b2 else None
+        return dx, dw1, db1, dw2, db2, None, None, gy if ctx.needs_input_grad[7] else None
+
+
+class Fp8MLP(torch.nn.Module):
+    """Two FP8 linears with an activation between (bf16 parameters).
+
+    features and hidden must be multiples of 16. forward(x, residual) adds a
+    bf16 residual (often x itself) in the second product's epilogue.
+    """
+
+    RINGS = 6
+
+    def __init__(self, features, hidden, bias=True, device=None, activation="gelu_tanh"):
+        super().__init__()
+        if features % 16 or hidden % 16:
+            raise ValueError("Fp8MLP needs features and hidden divisible by 16")
+        self.features, self.hidden, self.activation = features, hidden, activation
+        self._act = _act_code(activation)
+        kw = {"device": device, "dtype": torch.bfloat16}
+        self.weight1 = torch.nn.Parameter(torch.empty(hidden, features, **kw))
+        self.weight2 = torch.nn.Parameter(torch.empty(features, hidden, **kw))
+        self.bias1 = torch.nn.Parameter(torch.zeros(hidden, **kw)) if bias else None
+        self.bias2 = torch.nn.Parameter(torch.zeros(features, **kw)) if bias else None
+        self.register_buffer("fp8_rings", torch.zeros(self.RINGS, _RING_WORDS, dtype=torch.int32, device=device))
+        self._rings_ready = False
+        torch.nn.init.normal_(self.weight1, std=features ** -0.5)
+        torch.nn.init.normal_(self.weight2, std=hidden ** -0.5)
+
+    def reset_scaling(self):
+        """Reset the six rings (scale 1, empty history)."""
+        for i in range(self.RINGS):
+            fp8_ring_init(self.fp8_rings[i], 1.0)
+        self._rings_ready = True
+
+    def _load_from_state_dict(self, *args, **kwargs):
+        super()._load_from_state_dict(*args, **kwargs)
+        self._rings_ready = True  # restored rings are used as they are
+
+    def forward(self, x, residual=None):
+        if not self._rings_ready:
+            self.reset_scaling()
+        return Fp8MLPFunction.apply(x, self.weight1, self.bias1, self.weight2, self.bias2, self.fp8_rings, self._act,
+                                    residual)

@@ -490,6 +490,21 @@ FP8LITE_API fp8_status fp8_mm_experts(const uint8_t* a8, fp8_fmt fa, const uint8
                   int64_t M, int64_t N, int64_t K, int32_t experts, const int32_t* offsets,
                   const void* bias, fp8_act act, void* preact, void* out, void* stream);
 
+/* fp8_act_grad for the token-sorted rows of experts, in front of
+ * fp8_mm_experts' NN and TN products: rows [offsets[e], offsets[e+1]) belong to
+ * expert e, and dbias is bf16[experts][cols], each expert's own sums (zeros
+ * for one without rows). One ring and one scale for all. Rows of no expert
+ * count for nothing and keep what their out8 holds.
+ * experts    1 .. FP8_MM_MAX_EXPERTS
+ * offsets    device int32[experts + 1] as fp8_mm_experts'; others are limited
+ *            to [0, rows] and to the expert's first
+ * Other arguments and errors as fp8_act_grad; FP8_ERR_INVALID_ARG also for a
+ * NULL offsets or experts < 1, FP8_ERR_UNSUPPORTED for more experts. */
+FP8LITE_API fp8_status fp8_act_grad_experts(const void* g, const void* z, int64_t rows, int64_t cols,
+                        int32_t experts, const int32_t* offsets, fp8_act act, fp8_fmt fmt,
+                        fp8_ring* ring, uint32_t flags, uint8_t* out8, float* amax_out,
+                        float* scale_out, void* dbias, void* stream);
+
 /* Workspace bytes fp8_mm_ws needs for this problem and split_k on the
  * current device (split_k 0: for the library's own choice): 0 when that call
  * would not split, or for arguments fp8_mm_ws rejects. */

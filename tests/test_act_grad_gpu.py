@@ -167,3 +167,69 @@ def test_refusals():
     for kw in (dict(cols=12), dict(g=A + 2), dict(z=A + 8), dict(out=A + 8), dict(ring=S + 2), dict(scale=S + 130),
                dict(amax=S + 1), dict(db=S + 1)):
         assert _status(**kw) == AL, kw
+
+
+# ------------------------------------------------------------- rows of experts ---
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("counts", [[5], [300], [0, 5, 0, 0, 130, 1, 0], [127, 128, 129, 1, 255, 257, 64], [0] * 30 + [77],
+                                    [(7 * i) % 23 for i in range(512)], [2000, 1, 0, 3000]])
+@pytest.mark.parametrize("cols", [8, 264, 1040, 4096])
+@pytest.mark.parametrize("act", [R.NONE, R.SILU])
+def test_rows_of_experts(counts, cols, act):
+    gen = R.gen(cols + len(counts))
+    first, behind = (3, 9) if len(counts) % 2 else (0, 0)
+    off = torch.tensor([first] + counts).cumsum(0).to(torch.int32)
+    E, T, lo, hi = len(counts), int(off[-1]) + behind, int(off[0]), int(off[-1])
+    g, z = R.bf16(gen, (T, cols), 1e-3), R.bf16(gen, (T, cols), 2.0)
+    g[:lo] = 1.0  # rows of no expert: neither amax nor sums may see them
+    g[hi:] = float("nan")
+    ring = torch.empty(20, dtype=torch.int32, device="cuda")
+    s = float(torch.tensor(R.FMAX[1] / 2.5e-3, dtype=torch.float32))
+    fp8.fp8_ring_init(ring, s)
+    out = torch.full((T, cols), 9, dtype=torch.uint8, device="cuda")
+    amax, scale = (torch.empty(1, device="cuda") for _ in range(2))
+    db = torch.full((E, cols), 7.0, dtype=torch.bfloat16, device="cuda")
+    fp8.fp8_act_grad_experts(g, z, T, cols, E, off.cuda(), act, 1, ring, 0, out, amax, scale, db)
+    assert (out[:lo] == 9).all() and (out[hi:] == 9).all() and float(scale) == s
+    dz = g[lo:hi].double() * R.slope(z[lo:hi].double(), act)
+    e = g[lo:hi].double().abs() * (2.0 ** -20 * z[lo:hi].double().abs().clamp(min=1.0) if act else 0.0) + 2.0 ** -23 * dz.abs()
+    R.check_codes(out[lo:hi], 1, dz, e, s)
+    assert abs(float(amax) - float(dz.abs().max())) <= float(e.max())
+    for k in range(E):
+        a, b = int(off[k]) - lo, int(off[k + 1]) - lo
+        d = dz[a:b]
+        R.check_bf16(db[k], d.sum(0), e[a:b].sum(0) + (b - a) * 2.0 ** -24 * d.abs().sum(0), f"expert {k}")
+    h = fp8.fp8_ring_get(ring)
+    assert (h.idx, h.hist[0], h.amax_bits, h.ticket) == (1, float(amax), 0, 0)
+
+
+@pytest.mark.gpu
+def test_experts_without_rows_and_offsets_out_of_order():
+    ring = torch.empty(20, dtype=torch.int32, device="cuda")
+    fp8.fp8_ring_init(ring, 3.0)
+    g = R.bf16(R.gen(1), (50, 64))
+    amax, scale = (torch.empty(1, device="cuda") for _ in range(2))
+    db = torch.full((4, 64), 7.0, dtype=torch.bfloat16, device="cuda")
+    out = torch.full((50 * 64 + 256,), 9, dtype=torch.uint8, device="cuda")
+    fp8.fp8_act_grad_experts(g, None, 50, 64, 4, torch.zeros(5, dtype=torch.int32, device="cuda"), 0, 1, ring, 0, out, amax,
+                             scale, db)
+    assert (db == 0).all() and float(amax) == 0.0 and (out == 9).all()
+    bad = torch.tensor([-5, 20, 10, 10, 1 << 30], dtype=torch.int32, device="cuda")  # rows 0..20, none, none, 10..50
+    fp8.fp8_act_grad_experts(g, None, 50, 64, 4, bad, 0, 1, ring, 0, out, amax, scale, db)
+    assert (out[50 * 64:] == 9).all() and float(amax) == float(g.float().abs().max())
+    assert (db[1:3] == 0).all()
+
+
+def test_refusals_of_experts():
+    E, AL, U = fp8.FP8_ERR_INVALID_ARG, fp8.FP8_ERR_ALIGNMENT, fp8.FP8_ERR_UNSUPPORTED
+
+    def status(experts=4, offsets=S + 256, rows=8, cols=64, z=A, ring=S):
+        return fp8.raw_status("fp8_act_grad_experts", A, z, rows, cols, experts, offsets, 4, 1, ring, 0, A, None, S + 128,
+                              None, None)
+
+    assert status(experts=0) == E and status(offsets=None) == E and status(z=None) == E and status(ring=None) == E
+    assert status(rows=-1) == E and status(rows=1 << 31) == E
+    assert status(offsets=S + 2) == AL and status(cols=12) == AL
+    assert status(experts=513) == U
