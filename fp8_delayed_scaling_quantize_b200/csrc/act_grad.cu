@@ -3,7 +3,7 @@
 //
 // Bound by HBM: 5 bytes an element (g and z in bf16 read, one code written).
 //
-// Split: a cluster of up to 8 CTAs owns a strip of columns, its CTAs taking
+// Split: a cluster of up to 16 CTAs owns a strip of columns, its CTAs taking
 // row blocks in turn, so that a column's sum is finished inside the cluster:
 // each thread adds its rows, the warps meet in shared memory, and rank 0 adds
 // the other CTAs' sums through distributed shared memory. Every sum has one
@@ -29,7 +29,7 @@ constexpr int kThreads = 256;
 constexpr int kWarps = kThreads / 32;
 constexpr int kRows = 2;   // rows in flight per thread
 constexpr int kPerSm = 4;  // CTAs of an SM
-constexpr int kMaxRanks = 8;  // CTAs of a cluster
+constexpr int kMaxRanks = 16;  // CTAs of a cluster (more than 8 by opt-in)
 
 struct GradArgs {
     const uint4* g;
@@ -85,6 +85,28 @@ __device__ __forceinline__ float max_abs(float m, F2 v) {
     split(v, lo, hi);
     asm("max.abs.f32 %0, %0, %1, %2;" : "+f"(m) : "f"(lo), "f"(hi));
     return m;
+}
+
+// The cluster's amax (bmax: this CTA's, rank 0 of it) to the ring; the cluster
+// that holds the last ticket finishes the call. One thread.
+__device__ __forceinline__ void publish_amax(const GradArgs& a, float* bmax) {
+    float v = *bmax;
+    for (int r = 1; r < a.ranks; ++r) v = fmaxf(v, ld_cluster_f32(map_to_rank(smem_addr(bmax), uint32_t(r))));
+    fp8_ring* ring = a.ring;
+    if (v != 0.0f) atomicMax(&ring->amax_bits, __float_as_uint(v));
+    const uint32_t ticket = atom_add_acq_rel(&ring->ticket, 1u);
+    if (ticket != gridDim.x / a.ranks - 1) return;
+    volatile fp8_ring* rr = ring;
+    if (a.defer) {
+        if (a.amax_out) *a.amax_out = __uint_as_float(*reinterpret_cast<volatile uint32_t*>(&ring->amax_bits));
+    } else {
+        float h[FP8_RING_HISTORY];
+        const uint32_t idx = ring_read(rr, h);
+        const float top = __uint_as_float(atomicExch(&ring->amax_bits, 0u));
+        ring_fold(rr, h, idx, top, fmt_max(a.fmt));
+        if (a.amax_out) *a.amax_out = top;
+    }
+    rr->ticket = 0u;
 }
 
 // W: columns of a strip (64, 32 or 16).
@@ -168,89 +190,88 @@ __global__ void __launch_bounds__(kThreads, kPerSm) act_grad_kernel(const GradAr
             }
             n -= kRows;
         }
-        if (!a.dbias) continue;
-        // the block's column sums, then the cluster's: rank 0 adds them in rank order
+        // The block's column sums and, after its last range, its amax; then the
+        // cluster's: rank 0 takes them in rank order.
+        const bool last = e + a.parts >= a.experts;
+        if (!a.dbias && !last) continue;
+        if (a.dbias) {
 #pragma unroll
-        for (int i = 0; i < 4; ++i) {
-            float v0, v1;
-            split(sum[i], v0, v1);
+            for (int i = 0; i < 4; ++i) {
+                float v0, v1;
+                split(sum[i], v0, v1);
 #pragma unroll
-            for (int o = kTpr; o < 32; o <<= 1) {
-                v0 += __shfl_xor_sync(0xffffffffu, v0, o);
-                v1 += __shfl_xor_sync(0xffffffffu, v1, o);
-            }
-            if (lane < kTpr) {
-                part[warp][lane * 8 + 2 * i] = v0;
-                part[warp][lane * 8 + 2 * i + 1] = v1;
+                for (int o = kTpr; o < 32; o <<= 1) {
+                    v0 += __shfl_xor_sync(0xffffffffu, v0, o);
+                    v1 += __shfl_xor_sync(0xffffffffu, v1, o);
+                }
+                if (lane < kTpr) {
+                    part[warp][lane * 8 + 2 * i] = v0;
+                    part[warp][lane * 8 + 2 * i + 1] = v1;
+                }
             }
         }
+        if (last) {
+            griddep_launch();
+            const uint32_t bits = __reduce_max_sync(0xffffffffu, __float_as_uint(m));
+            if (lane == 0) wmax[warp] = bits;
+        }
         __syncthreads();
-        if (threadIdx.x < W) {
+        if (a.dbias && threadIdx.x < W) {
             float v = 0.0f;
 #pragma unroll
             for (int w = 0; w < kWarps; ++w) v += part[w][threadIdx.x];
             colsum[threadIdx.x] = v;
         }
+        if (last && threadIdx.x >= kThreads - 32) {
+            const uint32_t bits = __reduce_max_sync(0xffffffffu, lane < kWarps ? wmax[lane] : 0u);
+            if (lane == 0) bmax = __uint_as_float(bits);
+        }
         if (a.ranks > 1) cluster_sync();
-        if (rank == 0 && threadIdx.x < W) {
-            float v = colsum[threadIdx.x];
-            const uint32_t mine = smem_addr(&colsum[threadIdx.x]);
-            for (int r = 1; r < a.ranks; ++r) v += ld_cluster_f32(map_to_rank(mine, uint32_t(r)));
-            const int64_t c = strip * W + threadIdx.x;
-            if (c < a.pitch * 8) {
-                uint16_t h;
-                asm("cvt.rn.bf16.f32 %0, %1;" : "=h"(h) : "f"(v));
-                a.dbias[int64_t(e) * a.pitch * 8 + c] = h;
+        else             __syncthreads();
+        if (rank == 0) {
+            if (last && threadIdx.x == kThreads - 32) publish_amax(a, &bmax);
+            if (a.dbias && threadIdx.x < W) {
+                float v = colsum[threadIdx.x];
+                const uint32_t mine = smem_addr(&colsum[threadIdx.x]);
+                for (int r = 1; r < a.ranks; ++r) v += ld_cluster_f32(map_to_rank(mine, uint32_t(r)));
+                const int64_t c = strip * W + threadIdx.x;
+                if (c < a.pitch * 8) {
+                    uint16_t h;
+                    asm("cvt.rn.bf16.f32 %0, %1;" : "=h"(h) : "f"(v));
+                    a.dbias[int64_t(e) * a.pitch * 8 + c] = h;
+                }
             }
         }
-        // rank 0 has read every sum before they change, and the block its own parts
+        // rank 0 has read what the others hold before it changes or they leave
         if (a.ranks > 1) cluster_sync();
         else             __syncthreads();
     }
-    griddep_launch();
-    const uint32_t bits = __reduce_max_sync(0xffffffffu, __float_as_uint(m));
-    if (lane == 0) wmax[warp] = bits;
-    __syncthreads();
-    if (threadIdx.x == 0) {
-        uint32_t b = wmax[0];
-#pragma unroll
-        for (int w = 1; w < kWarps; ++w) b = max(b, wmax[w]);
-        bmax = __uint_as_float(b);
-    }
-    if (a.ranks > 1) cluster_sync();
-    if (rank == 0 && threadIdx.x == 0) {
-        float v = bmax;
-        for (int r = 1; r < a.ranks; ++r) v = fmaxf(v, ld_cluster_f32(map_to_rank(smem_addr(&bmax), uint32_t(r))));
-        fp8_ring* ring = a.ring;
-        if (v != 0.0f) atomicMax(&ring->amax_bits, __float_as_uint(v));
-        const uint32_t ticket = atom_add_acq_rel(&ring->ticket, 1u);
-        if (ticket == gridDim.x / a.ranks - 1) {
-            volatile fp8_ring* rr = ring;
-            if (a.defer) {
-                if (a.amax_out) *a.amax_out = __uint_as_float(*reinterpret_cast<volatile uint32_t*>(&ring->amax_bits));
-            } else {
-                float h[FP8_RING_HISTORY];
-                const uint32_t idx = ring_read(rr, h);
-                const float top = __uint_as_float(atomicExch(&ring->amax_bits, 0u));
-                ring_fold(rr, h, idx, top, fmt_max(a.fmt));
-                if (a.amax_out) *a.amax_out = top;
-            }
-            rr->ticket = 0u;
+}
+
+template <int ACT, int W>
+fp8_status launch_act(const GradArgs& a, int64_t strips, cudaStream_t st) {
+    auto kern = act_grad_kernel<ACT, W>;
+    if (a.ranks > 8) {
+        static bool allowed[64] = {false};
+        int dev = 0;
+        if (cudaGetDevice(&dev) != cudaSuccess || dev < 0 || dev >= 64) return FP8_ERR_CUDA;
+        if (!allowed[dev]) {
+            if (cudaFuncSetAttribute(kern, cudaFuncAttributeNonPortableClusterSizeAllowed, 1) != cudaSuccess)
+                return FP8_ERR_CUDA;
+            allowed[dev] = true;
         }
     }
-    if (a.ranks > 1) cluster_sync();  // no CTA leaves while rank 0 may still read its shared memory
+    return launch_pdl(kern, dim3(unsigned(strips * a.parts * a.ranks)), kThreads, 0, st, a.ranks, a);
 }
 
 template <int W>
 fp8_status launch_width(const GradArgs& a, int act, int64_t strips, cudaStream_t st) {
-    const dim3 grid(unsigned(strips * a.parts * a.ranks));
     switch (act) {
-        case FP8_ACT_NONE: return launch_pdl(act_grad_kernel<FP8_ACT_NONE, W>, grid, kThreads, 0, st, a.ranks, a);
-        case FP8_ACT_RELU: return launch_pdl(act_grad_kernel<FP8_ACT_RELU, W>, grid, kThreads, 0, st, a.ranks, a);
-        case FP8_ACT_GELU: return launch_pdl(act_grad_kernel<FP8_ACT_GELU, W>, grid, kThreads, 0, st, a.ranks, a);
-        case FP8_ACT_GELU_TANH:
-            return launch_pdl(act_grad_kernel<FP8_ACT_GELU_TANH, W>, grid, kThreads, 0, st, a.ranks, a);
-        default: return launch_pdl(act_grad_kernel<FP8_ACT_SILU, W>, grid, kThreads, 0, st, a.ranks, a);
+        case FP8_ACT_NONE:      return launch_act<FP8_ACT_NONE, W>(a, strips, st);
+        case FP8_ACT_RELU:      return launch_act<FP8_ACT_RELU, W>(a, strips, st);
+        case FP8_ACT_GELU:      return launch_act<FP8_ACT_GELU, W>(a, strips, st);
+        case FP8_ACT_GELU_TANH: return launch_act<FP8_ACT_GELU_TANH, W>(a, strips, st);
+        default:                return launch_act<FP8_ACT_SILU, W>(a, strips, st);
     }
 }
 
@@ -293,16 +314,21 @@ fp8_status act_grad_impl(const void* g, const void* z, int64_t rows, int64_t col
     // Strips of 64 columns (a row piece is one 128-byte line) unless they are
     // too few to give every SM two CTAs. Then as many CTAs as stay resident
     // together: experts first (their sums need no exchange), and to an expert
-    // as many CTAs of a cluster as its mean rows can feed.
+    // as many CTAs of a cluster as its mean rows can feed. Clusters of 16 only
+    // where the narrowest strips would leave SMs idle in clusters of 8:
+    // measured on B200 (SiLU, us, 8 against 16) 32768 x 128 20.9 -> 14.3, but
+    // 2048 x 1024 8.8 -> 11.4 and 32768 x 1040 42 -> 51 (fewer of them fit a
+    // GPC together).
     const auto strips = [&](int w) { return (cols + w - 1) / w; };
     const int64_t slots = kPerSm * 148;
-    const int w = strips(64) * experts * kMaxRanks >= 2 * 148 ? 64 : strips(32) * experts * kMaxRanks >= 2 * 148 ? 32 : 16;
+    const int w = strips(64) * experts * 8 >= 2 * 148 ? 64 : strips(32) * experts * 8 >= 2 * 148 ? 32 : 16;
+    const int max_ranks = strips(16) * experts * 8 < 148 ? kMaxRanks : 8;
     const int64_t n = strips(w);
     a.parts = int(n * experts <= slots ? experts : slots / n < 1 ? 1 : slots / n);
     const int64_t block_rows = kThreads / (w / 8);
     const int64_t blocks = (rows / experts + block_rows - 1) / block_rows;
     a.ranks = 1;
-    while (a.ranks < kMaxRanks && a.ranks < blocks && n * a.parts * a.ranks * 2 <= slots) a.ranks *= 2;
+    while (a.ranks < max_ranks && a.ranks < blocks && n * a.parts * a.ranks * 2 <= slots) a.ranks *= 2;
     cudaStream_t st = as_stream(stream);
     if (w == 64) return launch_width<64>(a, act, n, st);
     if (w == 32) return launch_width<32>(a, act, n, st);
