@@ -50,7 +50,7 @@ NT, NN, TN = 0, 1, 2
 
 
 KERNEL_SOURCES = {
-    "gemm": ("gemm.cu", "gemm_kernel.cuh", "sm100.cuh", "common.cuh"),
+    "gemm": ("gemm.cu", "gemm_kernel.cuh", "act.cuh", "sm100.cuh", "common.cuh"),
     "quantize": ("quantize.cu", "common.cuh"),
 }
 
