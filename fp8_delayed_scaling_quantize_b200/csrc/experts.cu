@@ -531,7 +531,10 @@ extern "C" fp8_status fp8_mm_experts(const uint8_t* a8, fp8_fmt fa, const uint8_
     if (N < 1 || (sum ? M : K) < 1 || rows < 0 || experts < 1) return FP8_ERR_INVALID_ARG;
     if (sb_stride != 0 && (sb_stride != 1 || sum)) return FP8_ERR_INVALID_ARG;
     if (sum && (bias || preact || act != FP8_ACT_NONE)) return FP8_ERR_INVALID_ARG;
-    if (!sa || !sb || !offsets || !b8 || (rows > 0 && !a8) || ((rows > 0 || sum) && !out)) return FP8_ERR_INVALID_ARG;
+    // without token rows the token matrices may be NULL
+    if (!sa || !sb || !offsets || (rows > 0 && !a8) || ((rows > 0 || !sum) && !b8) || ((rows > 0 || sum) && !out))
+        return FP8_ERR_INVALID_ARG;
+    if (preact && preact == out) return FP8_ERR_INVALID_ARG;
     if (experts > kMaxExperts || M >= (int64_t(1) << 31) || N >= (int64_t(1) << 31) || K >= (int64_t(1) << 31))
         return FP8_ERR_UNSUPPORTED;
     if ((sum ? M : K) % 16 != 0 || (layout != FP8_NT && N % 16 != 0)) return FP8_ERR_ALIGNMENT;

@@ -42,6 +42,9 @@ fp8_status mm_act_impl(const uint8_t* a8, fp8_fmt fa, const uint8_t* b8, fp8_fmt
     if (ok != FP8_OK) return ok;
     if (o.residual && (o.stride_r < 0 || (batch > 1 && o.stride_r != 0 && o.stride_r < M * N)))
         return FP8_ERR_INVALID_ARG;
+    // out and preact are written as the tiles come: only a residual laid out as out may be out
+    if (o.preact && (o.preact == out || o.preact == o.residual)) return FP8_ERR_INVALID_ARG;
+    if (o.residual == out && batch > 1 && o.stride_r != stride_c) return FP8_ERR_INVALID_ARG;
     if (!aligned(o.residual, 2) || !aligned(o.preact, 2)) return FP8_ERR_ALIGNMENT;
     if (o.out8 && (!aligned(o.ring, 4) || !aligned(o.scale, 4) || !aligned(o.amax, 4))) return FP8_ERR_ALIGNMENT;
     if (batch == 1) { stride_a = 0; stride_b = 0; }

@@ -461,7 +461,8 @@ __device__ __forceinline__ void act_stage_free(int lane) {
 
 // The staged block to global memory: by TMA, which clips what the map does
 // not hold, or row by row as far as rows and columns exist. PIECES: 16-byte
-// pieces of a staged row (4 for bf16, 2 for codes).
+// pieces of a staged row (4 for bf16, 2 for codes, which leave by TMA or
+// byte by byte).
 template <int PIECES>
 __device__ __forceinline__ void act_store(const ActTile& t, void* dst, const CUtensorMap* map, bool tma, bool vec,
                                           int col0, int lane) {
@@ -475,7 +476,7 @@ __device__ __forceinline__ void act_store(const ActTile& t, void* dst, const CUt
             tma_store_3d(map, t.stg, col0, t.row0, t.b);
             bulk_commit();
         }
-    } else if (vec) {
+    } else if (PIECES == 4 && vec) {
         __syncwarp();
         const int piece = lane % PIECES, col = col0 + piece * (16 / kElem);
 #pragma unroll

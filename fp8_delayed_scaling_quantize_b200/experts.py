@@ -13,6 +13,7 @@ all experts and the gradient, kept in `fp8_rings` with the state_dict.
 """
 
 import torch
+from torch.autograd.function import once_differentiable
 
 from . import (FP8_ACT_NONE, FP8_E4M3, FP8_E5M2, FP8_NN, FP8_NT, FP8_TN, fp8_act_grad_experts, fp8_mm_experts,
                fp8_ring_init)
@@ -45,6 +46,7 @@ class Fp8ExpertsFunction(torch.autograd.Function):
         return y
 
     @staticmethod
+    @once_differentiable
     def backward(ctx, gy):
         x8, w8, sx, sw, rings, offsets, z = ctx.saved_tensors
         T, N, K, E = ctx.dims
@@ -101,6 +103,7 @@ class Fp8Experts(torch.nn.Module):
         self._rings_ready = True  # restored rings are used as they are
 
     def forward(self, x, offsets):
-        if not self._rings_ready:
-            self.reset_scaling()
-        return Fp8ExpertsFunction.apply(x, offsets, self.weight, self.bias, self.fp8_rings, self._act)
+        with torch.cuda.device(x.device):  # the launches go to the current device's stream
+            if not self._rings_ready:
+                self.reset_scaling()
+            return Fp8ExpertsFunction.apply(x, offsets, self.weight, self.bias, self.fp8_rings, self._act)

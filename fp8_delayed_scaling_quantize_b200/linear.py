@@ -35,6 +35,7 @@ and torch would make that stream wait for the capture.
 """
 
 import torch
+from torch.autograd.function import once_differentiable
 
 from . import (FP8_ACT_GELU, FP8_ACT_GELU_TANH, FP8_ACT_NONE, FP8_ACT_RELU, FP8_ACT_SILU, FP8_E4M3, FP8_E5M2, FP8_NN,
                FP8_NT, FP8_RING_BYTES, FP8_TN, fp8_act_grad, fp8_bias_grad, fp8_mm, fp8_mm_act, fp8_mm_act_out8,
@@ -193,6 +194,7 @@ class Fp8LinearActFunction(torch.autograd.Function):
         return y.reshape(*x.shape[:-1], N)
 
     @staticmethod
+    @once_differentiable
     def backward(ctx, gy):
         x8, w8, sx, sw, rings, z = ctx.saved_tensors
         T, N, K = ctx.dims
@@ -250,7 +252,8 @@ class Fp8Linear(torch.nn.Module):
             self.reset_scaling()
         if self._act == FP8_ACT_NONE and residual is None:
             return Fp8LinearFunction.apply(x, self.weight, self.bias, self.fp8_rings)
-        return Fp8LinearActFunction.apply(x, self.weight, self.bias, self.fp8_rings, self._act, residual)
+        with torch.cuda.device(x.device):  # the launches go to the current device's stream
+            return Fp8LinearActFunction.apply(x, self.weight, self.bias, self.fp8_rings, self._act, residual)
 
 
 class Fp8MLPFunction(torch.autograd.Function):
@@ -288,6 +291,7 @@ class Fp8MLPFunction(torch.autograd.Function):
         return y.reshape(*x.shape[:-1], N)
 
     @staticmethod
+    @once_differentiable
     def backward(ctx, gy):
         x8, w18, h8, w28, sx, sw1, sh, sw2, rings, z = ctx.saved_tensors
         T, D, H, N = ctx.dims
@@ -347,7 +351,8 @@ class Fp8MLP(torch.nn.Module):
         self._rings_ready = True  # restored rings are used as they are
 
     def forward(self, x, residual=None):
-        if not self._rings_ready:
-            self.reset_scaling()
-        return Fp8MLPFunction.apply(x, self.weight1, self.bias1, self.weight2, self.bias2, self.fp8_rings, self._act,
-                                    residual)
+        with torch.cuda.device(x.device):  # the launches go to the current device's stream
+            if not self._rings_ready:
+                self.reset_scaling()
+            return Fp8MLPFunction.apply(x, self.weight1, self.bias1, self.weight2, self.bias2, self.fp8_rings, self._act,
+                                        residual)

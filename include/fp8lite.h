@@ -393,7 +393,9 @@ typedef enum fp8_act {
  * Any M and N that fp8_mm takes; with N and the strides multiples of 8 and
  * out, residual and preact 16-byte aligned the outputs leave as whole tiles
  * (faster). Never uses a workspace.
- * Errors: as fp8_mm; FP8_ERR_INVALID_ARG also for a bad act or stride_r. */
+ * Errors: as fp8_mm; FP8_ERR_INVALID_ARG also for a bad act or stride_r, a
+ * preact that is out or residual, and a residual that is out with another
+ * batch stride. */
 FP8LITE_API fp8_status fp8_mm_act(const uint8_t* a8, fp8_fmt fa, const uint8_t* b8, fp8_fmt fb,
                   const float* sa, const float* sb, fp8_layout layout,
                   int64_t M, int64_t N, int64_t K, int64_t batch,
@@ -406,7 +408,8 @@ FP8LITE_API fp8_status fp8_mm_act(const uint8_t* a8, fp8_fmt fa, const uint8_t* 
  * fp8_mm_out8's: out8[b,i,j] = sat_rne_out_fmt( fp32(act(z[b,i,j]) * s) ) with
  * s = out_ring->scale as it stood before the call, and the amax of |act(z)|
  * folded into out_ring. preact as fp8_mm_act; there is no residual.
- * Errors: as fp8_mm_out8; FP8_ERR_INVALID_ARG also for a bad act. */
+ * Errors: as fp8_mm_out8; FP8_ERR_INVALID_ARG also for a bad act and for a
+ * preact that is out8. */
 FP8LITE_API fp8_status fp8_mm_act_out8(const uint8_t* a8, fp8_fmt fa, const uint8_t* b8, fp8_fmt fb,
                   const float* sa, const float* sb, fp8_layout layout,
                   int64_t M, int64_t N, int64_t K, int64_t batch,
@@ -481,7 +484,7 @@ FP8LITE_API fp8_status fp8_act_grad(const void* g, const void* z, int64_t rows, 
  *            buffer. With N a multiple of 8 and out and preact 16-byte
  *            aligned the outputs leave as whole tiles (faster).
  * No workspace. Errors: FP8_ERR_INVALID_ARG (also bias, preact, an activation
- * or sb_stride 1 in TN), FP8_ERR_ALIGNMENT, FP8_ERR_UNSUPPORTED (a size >= 2^31
+ * or sb_stride 1 in TN, and a preact that is out), FP8_ERR_ALIGNMENT, FP8_ERR_UNSUPPORTED (a size >= 2^31
  * or more experts), FP8_ERR_CUDA. A bounded device wait that gives up is
  * reported by fp8_last_device_error. */
 #define FP8_MM_MAX_EXPERTS 512

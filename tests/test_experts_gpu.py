@@ -175,7 +175,7 @@ def test_no_rows():
     b = torch.zeros(3, 32, 16, dtype=torch.uint8, device="cuda")
     fp8.fp8_mm_experts(None, 0, b, 0, sa, sa, 0, NT, 0, 32, 16, 3, off, None, R.NONE, None, None)
     dw = torch.full((3, 32, 16), 7.0, dtype=torch.bfloat16, device="cuda")
-    fp8.fp8_mm_experts(None, 0, b, 0, sa, sa, 0, TN, 32, 16, 0, 3, off, None, R.NONE, None, dw)
+    fp8.fp8_mm_experts(None, 0, None, 0, sa, sa, 0, TN, 32, 16, 0, 3, off, None, R.NONE, None, dw)
     assert (dw == 0).all()
     out = torch.full((4, 32), 7.0, dtype=torch.bfloat16, device="cuda")  # rows, but none of an expert
     a = torch.zeros(4, 16, dtype=torch.uint8, device="cuda")
@@ -219,10 +219,10 @@ def test_refusals():
     for kw in (dict(fa=2), dict(layout=3), dict(act=5), dict(act=-1), dict(M=-1), dict(N=0), dict(K=0), dict(experts=0),
                dict(offsets=None), dict(a8=None), dict(b8=None), dict(sa=None), dict(sb=None), dict(out=None),
                dict(stride=2), dict(stride=-1), dict(layout=TN, stride=1), dict(layout=TN, bias=A),
-               dict(layout=TN, act=1), dict(layout=TN, preact=A), dict(layout=TN, M=0), dict(layout=TN, K=-1)):
+               dict(layout=TN, act=1), dict(layout=TN, preact=A), dict(preact=A), dict(layout=TN, M=0), dict(layout=TN, K=-1)):
         assert _status(**kw) == E, kw
     for kw in (dict(K=24), dict(layout=NN, K=24), dict(layout=NN, N=24), dict(layout=TN, M=24), dict(layout=TN, N=24),
-               dict(a8=A + 8), dict(b8=A + 8), dict(out=A + 1), dict(preact=A + 1), dict(bias=A + 1), dict(sa=S + 2),
+               dict(a8=A + 8), dict(b8=A + 8), dict(out=A + 1), dict(preact=A + 4097), dict(bias=A + 1), dict(sa=S + 2),
                dict(sb=S + 2), dict(offsets=S + 2)):
         assert _status(**kw) == AL, kw
     for kw in (dict(experts=513), dict(M=1 << 31), dict(N=1 << 31), dict(K=1 << 31)):

@@ -240,6 +240,32 @@ def test_experts_are_their_calls(act, counts, K, N, bias):
         assert torch.equal(layer.fp8_rings, rings)
 
 
+def test_experts_empty_batch_no_grad_and_state_dict():
+    from fp8_delayed_scaling_quantize_b200.experts import Fp8Experts
+    a = Fp8Experts(3, 64, 32, device="cuda", activation="relu")
+    off = torch.zeros(4, dtype=torch.int32, device="cuda")
+    e = torch.empty(0, 64, dtype=torch.bfloat16, device="cuda", requires_grad=True)
+    a(e, off).sum().backward()
+    assert e.grad.shape == (0, 64) and all((p.grad == 0).all() for p in a.parameters())
+    x = R.bf16(R.gen(2), (30, 64))
+    off.copy_(torch.tensor([0, 10, 10, 30], dtype=torch.int32))
+    with torch.no_grad():
+        y = a(x, off)
+    assert y.grad_fn is None
+    b = Fp8Experts(3, 64, 32, device="cuda", activation="relu")
+    b.load_state_dict(a.state_dict())
+    _same(a(x, off).detach(), b(x, off).detach())
+
+
+def test_a_second_derivative_is_refused():
+    from fp8_delayed_scaling_quantize_b200.linear import Fp8MLP
+    mlp = Fp8MLP(64, 64, device="cuda")
+    x = R.bf16(R.gen(2), (8, 64)).requires_grad_(True)
+    (dx,) = torch.autograd.grad(mlp(x).sum(), x, create_graph=True)
+    with pytest.raises(RuntimeError):
+        dx.sum().backward()
+
+
 def _route(x, router, top):
     """Token-sorted copies for the top experts of each token: (rows, offsets, source token, gate)."""
     p, e = torch.softmax(x.float() @ router, -1).topk(top, -1)

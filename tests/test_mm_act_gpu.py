@@ -241,6 +241,9 @@ def test_refusals():
     assert _act(residual=A, stride_r=-8) == E
     assert _act(residual=A, batch=2, stride_c=128 * 128, stride_r=128) == E
     assert _act(batch=2, stride_c=8) == E
+    assert _act(preact=A + 4096) == E and _act(preact=A, residual=A) == E  # preact is out, preact is residual
+    assert _act(residual=A + 4096, batch=2, stride_c=128 * 128, stride_r=0) == E  # in place under another stride
+    assert _out8(preact=A + 4096) == E
     assert _act(residual=A + 1) == AL and _act(preact=A + 1) == AL and _act(out=A + 2) == AL
     assert _act(K=24) == AL and _act(a8=A + 8) == AL
     assert _act(M=1 << 31) == U
