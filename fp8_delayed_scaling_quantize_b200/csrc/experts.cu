@@ -517,6 +517,27 @@ inline bool use_pair(bool sum, int64_t rows, int64_t M, int64_t N, int64_t K, in
     return N > 128 && kb >= 16 && (sum ? M > BM : rows >= 1024 * experts);
 }
 
+// Whether 128-wide tiles serve NT and NN, for about `m` rows of tiles and `kb`
+// k-blocks each: rounds of the grid times the k-blocks at the tile's rate, plus
+// the last epilogue (the constants of choose_tile). Measured on B200 (us, 256
+// wide against 128): 4 experts of 100 rows, 2048 x 2048 12.5 -> 9.9, of 250
+// rows, 1024 x 1024 8.8 -> 7.3; but 8 of 500 rows, 2048 x 1024 14.6 -> 17.2.
+inline bool narrow_rows(double m, int64_t N, double kb) {
+    auto cost = [&](int bn, double t_k, double t_epi) {
+        const double rounds = m * double((N + bn - 1) / bn) / double(sm_count());
+        const double whole = rounds < 4.0 ? double(int64_t(rounds + 0.999)) : rounds;
+        return (whole < 1.0 ? 1.0 : whole) * kb * t_k + t_epi;
+    };
+    return cost(128, 0.40, 1.0) < cost(256, 0.48, 2.0);
+}
+
+// TN writes more than it multiplies, and wide tiles write faster: 128-wide ones
+// only where 256-wide ones would leave half of the SMs without any (2 experts,
+// 1024 x 512 5.9 -> 5.1 us; 16 of 512 x 512, 128 wide tiles, 6.2 -> 6.7).
+inline bool narrow_sum(int64_t experts, int64_t M, int64_t N) {
+    return experts * ((M + BM - 1) / BM) * ((N + 255) / 256) * 2 <= sm_count();
+}
+
 }  // namespace
 }  // namespace fp8lite
 
@@ -569,17 +590,18 @@ extern "C" fp8_status fp8_mm_experts(const uint8_t* a8, fp8_fmt fa, const uint8_
         return rows / tile + with_rows;
     };
     constexpr int64_t kMost = int64_t(1) << 31;
-    constexpr int BN = 256;
+    const bool pair = use_pair(sum, rows, M, N, K, experts);
     if (sum) {
-        const bool pair = use_pair(sum, rows, M, N, K, experts);
+        const int bn = pair || !narrow_sum(experts, M, N) ? 256 : 128;
         p.m_tiles = int((M + BM * (pair ? 2 : 1) - 1) / (BM * (pair ? 2 : 1)));
-        p.n_tiles = int((N + BN - 1) / BN);
+        p.n_tiles = int((N + bn - 1) / bn);
         const int64_t units = int64_t(experts) * p.m_tiles * p.n_tiles;
         if (units >= kMost) return FP8_ERR_UNSUPPORTED;
         if (!make_block_map(&ta, a8, M, rows) || !make_block_map(&tb, b8, N, rows)) return FP8_ERR_CUDA;
         if (p.fast && !make_out_map(&tc, out, N, M, experts, uint64_t(M) * N * 2, 32)) return FP8_ERR_CUDA;
-        if (pair) return launch_experts<BN, kSumTN, 6, false, 2>(ta, tb, tc, tz, p, fa, fb, units, st);
-        return launch_experts<BN, kSumTN, 4, false>(ta, tb, tc, tz, p, fa, fb, units, st);
+        if (pair) return launch_experts<256, kSumTN, 6, false, 2>(ta, tb, tc, tz, p, fa, fb, units, st);
+        if (bn == 256) return launch_experts<256, kSumTN, 4, false>(ta, tb, tc, tz, p, fa, fb, units, st);
+        return launch_experts<128, kSumTN, 6, false>(ta, tb, tc, tz, p, fa, fb, units, st);
     }
     const bool nn = layout == FP8_NN;
     // Few rows an expert: swapped tiles of 16 or 32 token rows
@@ -598,19 +620,24 @@ extern "C" fp8_status fp8_mm_experts(const uint8_t* a8, fp8_fmt fa, const uint8_
         return nn ? launch_experts<32, kRowsNN, 9, true>(ta, tb, tc, tz, p, fa, fb, units, st)
                   : launch_experts<32, kRowsNT, 9, true>(ta, tb, tc, tz, p, fa, fb, units, st);
     }
-    const bool pair = use_pair(sum, rows, M, N, K, experts);
-    p.n_tiles = int((N + BN - 1) / BN);
+    // an expert's last tile is half empty on average
+    const double m_tiles = double(rows) / BM + 0.5 * double(experts < rows ? experts : rows);
+    const int bn = pair || !narrow_rows(m_tiles, N, double(p.k_blocks)) ? 256 : 128;
+    p.n_tiles = int((N + bn - 1) / bn);
     const int64_t units = most(BM * (pair ? 2 : 1)) * p.n_tiles;
     if (units >= kMost) return FP8_ERR_UNSUPPORTED;
     const bool ok = make_map(&ta, a8, K, rows, 1, 0, BK, BM) &&
                     (nn ? make_map(&tb, b8, N, K, experts, uint64_t(N) * K, 128, BK)
-                        : make_map(&tb, b8, K, N, experts, uint64_t(N) * K, BK, pair ? BN / 2 : BN));
+                        : make_map(&tb, b8, K, N, experts, uint64_t(N) * K, BK, uint32_t(pair ? bn / 2 : bn)));
     if (!ok) return FP8_ERR_CUDA;
     if (p.fast && !make_out_map(&tc, out, N, rows, 1, 0, 32)) return FP8_ERR_CUDA;
     if (p.fast && preact && !make_out_map(&tz, preact, N, rows, 1, 0, 32)) return FP8_ERR_CUDA;
     if (pair)
-        return nn ? launch_experts<BN, kRowsNN, 6, false, 2>(ta, tb, tc, tz, p, fa, fb, units, st)
-                  : launch_experts<BN, kRowsNT, 6, false, 2>(ta, tb, tc, tz, p, fa, fb, units, st);
-    return nn ? launch_experts<BN, kRowsNN, 4, false>(ta, tb, tc, tz, p, fa, fb, units, st)
-              : launch_experts<BN, kRowsNT, 4, false>(ta, tb, tc, tz, p, fa, fb, units, st);
+        return nn ? launch_experts<256, kRowsNN, 6, false, 2>(ta, tb, tc, tz, p, fa, fb, units, st)
+                  : launch_experts<256, kRowsNT, 6, false, 2>(ta, tb, tc, tz, p, fa, fb, units, st);
+    if (bn == 256)
+        return nn ? launch_experts<256, kRowsNN, 4, false>(ta, tb, tc, tz, p, fa, fb, units, st)
+                  : launch_experts<256, kRowsNT, 4, false>(ta, tb, tc, tz, p, fa, fb, units, st);
+    return nn ? launch_experts<128, kRowsNN, 6, false>(ta, tb, tc, tz, p, fa, fb, units, st)
+              : launch_experts<128, kRowsNT, 6, false>(ta, tb, tc, tz, p, fa, fb, units, st);
 }
