@@ -13,12 +13,11 @@
 //  * A tile that reaches past its expert's last row loads the next expert's
 //    rows too; their results are dropped at the store, which writes such a
 //    tile in 16-byte row pieces and a whole tile by TMA.
-//  * In TN the rows are the contraction, so a block of 128 may hold no row of
-//    another expert. Its tensor map has two row dimensions of the same pitch:
-//    the block's first row, and 128 rows from there. A block of t < 128 rows
-//    starts at row t - 128 of the second: rows below 0 are out of bounds and
-//    arrive as zeros, the last t are the expert's (both operands alike, so
-//    the order of the sum is all that changes).
+//  * In TN the rows are the contraction, and an expert's last block of 128 may
+//    hold rows of the next one. Of a block of t < 128 rows only the ceil(t / 32)
+//    MMA slices (32 rows each) that hold rows of the expert are issued, and the
+//    MMA warp first clears the last slice's other rows in shared memory, in
+//    both operands: a NaN code in either would reach the sum through a zero.
 //  * Few rows an expert (swapped): the weight's columns run along the tensor
 //    core's 128 rows and 16 or 32 token rows are its N, so that a weight tile
 //    is read once for all of them and no operand is padded to 128 tokens.
@@ -58,7 +57,7 @@ struct ExpertParams {
 // One tile of work.
 struct Item {
     int e;          // expert
-    int m0, m_end;  // ROWS: first row of the tile and the expert's end; SUM: first row of the output, M
+    int m0, m_end;  // ROWS: first row of the tile and the expert's end; SUM: first row of the tile in the output, M
     int n0;         // first output column (swapped: of 128)
     int kbs;        // k-blocks
     int k_row, k_end;  // SUM: the expert's rows
@@ -204,6 +203,15 @@ __device__ __forceinline__ Item item_of(Experts<TILE>& x, const ExpertParams& p,
     return it;
 }
 
+constexpr int kSliceRows = 32;  // K of one MMA
+
+// Rows [from, to) of a 128-column operand tile, 128 bytes each in shared
+// memory (the swizzle stays within a row), become zeros: a whole warp.
+__device__ __forceinline__ void clear_rows(uint8_t* tile, int from, int to, int lane) {
+    for (int i = from * 128 + lane * 16; i < to * 128; i += 32 * 16)
+        *reinterpret_cast<uint4*>(tile + i) = make_uint4(0u, 0u, 0u, 0u);
+}
+
 // KIND, SWAP: see the head of the file. BN: output columns of a tile, or
 // token rows of a swapped one. CTAS = 2: a pair of CTAs on 256 x BN tiles
 // (cta_group::2): each loads its 128 rows of A and half of B and writes its
@@ -214,6 +222,7 @@ expert_kernel(const __grid_constant__ CUtensorMap tm_a, const __grid_constant__ 
               const __grid_constant__ CUtensorMap tm_c, const __grid_constant__ CUtensorMap tm_z, const ExpertParams p) {
     using L = Smem<BN, STAGES, CTAS, SWAP ? 3 : 4>;
     static_assert(CTAS == 1 || (BN == 256 && !SWAP), "a pair's half of an MN-major B is one 128-byte atom");
+    static_assert(CTAS == 1 || KIND != kSumTN, "the leader's MMA warp could not clear the other CTA's rows");
     constexpr int ET = epi_threads(true, SWAP);
     constexpr int TILE = SWAP ? BN : BM * CTAS;
     // majors of the MMA's operands: K-major unless the stored rows run along K
@@ -293,10 +302,9 @@ expert_kernel(const __grid_constant__ CUtensorMap tm_a, const __grid_constant__ 
                     const int m0 = it.m0 + int(rank) * BM, n0 = it.n0 + int(rank) * (BN / CTAS);
                     if constexpr (KIND == kSumTN) {
                         const int first = it.k_row + kb * BK;
-                        const int r0 = min(it.k_end - first, BK) - BK;  // 0, or negative in the last block
-                        load(da, &tm_a, m0, r0, first);
+                        load(da, &tm_a, m0, first, 0);
 #pragma unroll
-                        for (int h = 0; h < kAtoms; ++h) load(db + h * 128 * BK, &tm_b, n0 + h * 128, r0, first);
+                        for (int h = 0; h < kAtoms; ++h) load(db + h * 128 * BK, &tm_b, n0 + h * 128, first, 0);
                     } else if constexpr (SWAP) {
                         if (A_MN) load(da, &tm_b, it.n0, kb * BK, it.e);
                         else      load(da, &tm_b, kb * BK, it.n0, it.e);
@@ -336,10 +344,30 @@ expert_kernel(const __grid_constant__ CUtensorMap tm_a, const __grid_constant__ 
             tc_fence_after();
             for (int kb = 0; kb < it.kbs; ++kb) {
                 if (!wait_bounded_warp(bar_full + 8 * stage, phase)) { ok = false; break; }
+                const uint64_t a_desc = a_desc0 + uint64_t(stage) * (L::kABytes >> 4);
+                const uint64_t b_desc = b_desc0 + uint64_t(stage) * (L::kBBytes >> 4);
+                int left = BK;  // SUM: the expert's rows in the block
+                if constexpr (KIND == kSumTN) {
+                    left = it.k_end - (it.k_row + kb * BK);
+                    if (left < BK && left % kSliceRows != 0) {
+                        const int to = (left + kSliceRows - 1) / kSliceRows * kSliceRows;
+                        clear_rows(smem + stage * L::kABytes, left, to, lane);
+#pragma unroll
+                        for (int h = 0; h < BN / 128; ++h)
+                            clear_rows(smem + STAGES * L::kABytes + stage * L::kBBytes + h * 128 * BK, left, to, lane);
+                        fence_proxy_async_smem();
+                        __syncwarp();
+                    }
+                }
                 if (issuer) {
-                    mma_kblock_f8f6f4<CTAS>(tmem_base + buf * BN, a_desc0 + uint64_t(stage) * (L::kABytes >> 4),
-                                         b_desc0 + uint64_t(stage) * (L::kBBytes >> 4), A_MN ? 256u : 2u,
-                                         B_MN ? 256u : 2u, p.idesc, kb != 0);
+                    if (KIND == kSumTN && left < BK) {
+                        for (int k = 0; k * kSliceRows < left; ++k)
+                            mma_slice_f8f6f4(tmem_base + buf * BN, a_desc + uint64_t(k) * 256u, b_desc + uint64_t(k) * 256u,
+                                             p.idesc, (kb | k) != 0);
+                    } else {
+                        mma_kblock_f8f6f4<CTAS>(tmem_base + buf * BN, a_desc, b_desc, A_MN ? 256u : 2u, B_MN ? 256u : 2u,
+                                                p.idesc, kb != 0);
+                    }
                     if (CTAS == 2) mma_commit_pair(bar_empty + 8 * stage);
                     else           mma_commit(bar_empty + 8 * stage);
                 }
@@ -471,20 +499,6 @@ expert_kernel(const __grid_constant__ CUtensorMap tm_a, const __grid_constant__ 
     }
 }
 
-// Token rows as blocks of up to 128 that may start at any row: (columns, row
-// within the block, first row), both row dimensions one row apart.
-bool make_block_map(CUtensorMap* map, const void* base, uint64_t cols, uint64_t rows) {
-    EncodeTiledFn fn = encode_fn();
-    if (!fn) return false;
-    cuuint64_t dims[3] = {cols, uint64_t(BK), rows};
-    cuuint64_t strides[2] = {cols, cols};
-    cuuint32_t box[3] = {128, uint32_t(BK), 1};
-    cuuint32_t estr[3] = {1, 1, 1};
-    return fn(map, CU_TENSOR_MAP_DATA_TYPE_UINT8, 3, const_cast<void*>(base), dims, strides, box, estr,
-              CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
-              CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
-}
-
 template <int BN, int KIND, int STAGES, bool SWAP, int CTAS = 1>
 fp8_status launch_experts(const CUtensorMap& ta, const CUtensorMap& tb, const CUtensorMap& tc, const CUtensorMap& tz,
                           ExpertParams p, int fa, int fb, int64_t most_units, cudaStream_t st) {
@@ -505,16 +519,14 @@ fp8_status launch_experts(const CUtensorMap& ta, const CUtensorMap& tb, const CU
     return launch_pdl(kern, grid, 64 + epi_threads(true, SWAP), L::kAlloc, st, CTAS, ta, tb, tc, tz, p);
 }
 
-// Whether an SM pair's 256 x 256 tiles serve the call. They take in less per
+// Whether an SM pair's 256 x 256 tiles serve NT and NN. They take in less per
 // MMA but pad an expert's last rows to 256 and halve the grid's grain, so they
 // pay with many rows an expert and a long main loop. Measured on B200 (us, one
 // SM against pairs): 8 experts of 2048 rows, 4096 x 2048 121 -> 111, its dX
-// (32 k-blocks) 114 -> 107, its dW (16) 119 -> 110; but with 8 k-blocks 67 ->
-// 71 even for one expert of 16384 rows, and 32 experts of 512 rows 82 -> 92,
-// dX 68.5 -> 70.9, dW (4) 97 -> 114.
-inline bool use_pair(bool sum, int64_t rows, int64_t M, int64_t N, int64_t K, int64_t experts) {
-    const int64_t kb = (sum ? rows / experts : K) / BK;
-    return N > 128 && kb >= 16 && (sum ? M > BM : rows >= 1024 * experts);
+// (32 k-blocks) 114 -> 107; but with 8 k-blocks 67 -> 71 even for one expert of
+// 16384 rows, and 32 experts of 512 rows 82 -> 92, dX 68.5 -> 70.9.
+inline bool use_pair(int64_t rows, int64_t N, int64_t K, int64_t experts) {
+    return N > 128 && K / BK >= 16 && rows >= 1024 * experts;
 }
 
 // Whether 128-wide tiles serve NT and NN, for about `m` rows of tiles and `kb`
@@ -533,7 +545,7 @@ inline bool narrow_rows(double m, int64_t N, double kb) {
 
 // TN writes more than it multiplies, and wide tiles write faster: 128-wide ones
 // only where 256-wide ones would leave half of the SMs without any (2 experts,
-// 1024 x 512 5.9 -> 5.1 us; 16 of 512 x 512, 128 wide tiles, 6.2 -> 6.7).
+// 1024 x 512, 32 wide tiles: 5.9 -> 5.1 us; 16 of 512 x 512, 128 of them: 6.2 -> 6.7).
 inline bool narrow_sum(int64_t experts, int64_t M, int64_t N) {
     return experts * ((M + BM - 1) / BM) * ((N + 255) / 256) * 2 <= sm_count();
 }
@@ -590,16 +602,14 @@ extern "C" fp8_status fp8_mm_experts(const uint8_t* a8, fp8_fmt fa, const uint8_
         return rows / tile + with_rows;
     };
     constexpr int64_t kMost = int64_t(1) << 31;
-    const bool pair = use_pair(sum, rows, M, N, K, experts);
     if (sum) {
-        const int bn = pair || !narrow_sum(experts, M, N) ? 256 : 128;
-        p.m_tiles = int((M + BM * (pair ? 2 : 1) - 1) / (BM * (pair ? 2 : 1)));
+        const int bn = narrow_sum(experts, M, N) ? 128 : 256;
+        p.m_tiles = int((M + BM - 1) / BM);
         p.n_tiles = int((N + bn - 1) / bn);
         const int64_t units = int64_t(experts) * p.m_tiles * p.n_tiles;
         if (units >= kMost) return FP8_ERR_UNSUPPORTED;
-        if (!make_block_map(&ta, a8, M, rows) || !make_block_map(&tb, b8, N, rows)) return FP8_ERR_CUDA;
+        if (!make_map(&ta, a8, M, rows, 1, 0, 128, BK) || !make_map(&tb, b8, N, rows, 1, 0, 128, BK)) return FP8_ERR_CUDA;
         if (p.fast && !make_out_map(&tc, out, N, M, experts, uint64_t(M) * N * 2, 32)) return FP8_ERR_CUDA;
-        if (pair) return launch_experts<256, kSumTN, 6, false, 2>(ta, tb, tc, tz, p, fa, fb, units, st);
         if (bn == 256) return launch_experts<256, kSumTN, 4, false>(ta, tb, tc, tz, p, fa, fb, units, st);
         return launch_experts<128, kSumTN, 6, false>(ta, tb, tc, tz, p, fa, fb, units, st);
     }
@@ -620,6 +630,7 @@ extern "C" fp8_status fp8_mm_experts(const uint8_t* a8, fp8_fmt fa, const uint8_
         return nn ? launch_experts<32, kRowsNN, 9, true>(ta, tb, tc, tz, p, fa, fb, units, st)
                   : launch_experts<32, kRowsNT, 9, true>(ta, tb, tc, tz, p, fa, fb, units, st);
     }
+    const bool pair = use_pair(rows, N, K, experts);
     // an expert's last tile is half empty on average
     const double m_tiles = double(rows) / BM + 0.5 * double(experts < rows ? experts : rows);
     const int bn = pair || !narrow_rows(m_tiles, N, double(p.k_blocks)) ? 256 : 128;

@@ -225,6 +225,17 @@ __device__ __forceinline__ void mma_kblock_f8f6f4(uint32_t tmem_d, uint64_t ades
             : "memory");
 }
 
+// One of them: a K = 32 slice, for a block that does not hold four.
+__device__ __forceinline__ void mma_slice_f8f6f4(uint32_t tmem_d, uint64_t adesc, uint64_t bdesc, uint32_t idesc,
+                                                 uint32_t accumulate) {
+    asm volatile(
+        "{\n\t.reg .pred p;\n\t"
+        "setp.ne.b32 p, %4, 0;\n\t"
+        "tcgen05.mma.cta_group::1.kind::f8f6f4 [%0], %1, %2, %3, p;\n\t}" ::"r"(tmem_d),
+        "l"(adesc), "l"(bdesc), "r"(idesc), "r"(accumulate)
+        : "memory");
+}
+
 // Arrive once on this CTA's mbarrier `bar` when every tcgen05 op this thread
 // issued so far is done.
 __device__ __forceinline__ void mma_commit(uint32_t bar) {
