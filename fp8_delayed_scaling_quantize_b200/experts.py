@@ -17,7 +17,7 @@ from torch.autograd.function import once_differentiable
 
 from . import (FP8_ACT_NONE, FP8_E4M3, FP8_E5M2, FP8_NN, FP8_NT, FP8_TN, fp8_act_grad_experts, fp8_mm_experts,
                fp8_ring_init)
-from .linear import _RING_WORDS, _act_code, _quantize_many, _rows_of
+from .linear import _RING_WORDS, _act_code, _on_input, _quantize_many, _rows_of
 
 
 class Fp8ExpertsFunction(torch.autograd.Function):
@@ -103,7 +103,8 @@ class Fp8Experts(torch.nn.Module):
         self._rings_ready = True  # restored rings are used as they are
 
     def forward(self, x, offsets):
-        with torch.cuda.device(x.device):  # the launches go to the current device's stream
+        # the launches go to the current device's stream
+        with torch.cuda.device(_on_input(x, self.fp8_rings, self.weight, self.bias)):
             if not self._rings_ready:
                 self.reset_scaling()
             return Fp8ExpertsFunction.apply(x, offsets, self.weight, self.bias, self.fp8_rings, self._act)

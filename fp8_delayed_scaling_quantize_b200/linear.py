@@ -62,6 +62,18 @@ def _rows_of(x, features, what):
     return x.reshape(-1, features).contiguous()
 
 
+def _on_input(x, rings, *params):
+    """What the kernels take by address: bf16 parameters and the rings on the input's GPU. Returns that device."""
+    for t in params:
+        if t is not None and t.dtype != torch.bfloat16:
+            raise TypeError("parameters and residual must be bf16")
+    if not x.is_cuda:
+        raise ValueError("the input must be on a GPU")
+    if any(t is not None and t.device != x.device for t in (rings, *params)):
+        raise ValueError(f"parameters and rings must be on the input's device {x.device}")
+    return x.device
+
+
 def _quantize(t, n, fmt, ring):
     q = torch.empty(n, dtype=torch.uint8, device=t.device)
     amax = torch.empty(1, dtype=torch.float32, device=t.device)
@@ -248,11 +260,14 @@ class Fp8Linear(torch.nn.Module):
         self._rings_ready = True  # restored rings are used as they are
 
     def forward(self, x, residual=None):
-        if not self._rings_ready:
-            self.reset_scaling()
         if self._act == FP8_ACT_NONE and residual is None:
+            if not self._rings_ready:
+                self.reset_scaling()
             return Fp8LinearFunction.apply(x, self.weight, self.bias, self.fp8_rings)
-        with torch.cuda.device(x.device):  # the launches go to the current device's stream
+        # the launches go to the current device's stream
+        with torch.cuda.device(_on_input(x, self.fp8_rings, self.weight, self.bias, residual)):
+            if not self._rings_ready:
+                self.reset_scaling()
             return Fp8LinearActFunction.apply(x, self.weight, self.bias, self.fp8_rings, self._act, residual)
 
 
@@ -351,7 +366,8 @@ class Fp8MLP(torch.nn.Module):
         self._rings_ready = True  # restored rings are used as they are
 
     def forward(self, x, residual=None):
-        with torch.cuda.device(x.device):  # the launches go to the current device's stream
+        params = (self.weight1, self.weight2, self.bias1, self.bias2, residual)
+        with torch.cuda.device(_on_input(x, self.fp8_rings, *params)):  # the launches go to the current device's stream
             if not self._rings_ready:
                 self.reset_scaling()
             return Fp8MLPFunction.apply(x, self.weight1, self.bias1, self.weight2, self.bias2, self.fp8_rings, self._act,
