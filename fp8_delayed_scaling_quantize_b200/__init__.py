@@ -108,6 +108,7 @@ def _load():
                                 P]),
         "fp8_mm_experts": (I, [P, I, P, I, P, P, ctypes.c_int32, I, I64, I64, I64, ctypes.c_int32, P, P, I, P, P, P]),
         "fp8_act_grad_experts": (I, [P, P, I64, I64, ctypes.c_int32, P, I, I, P, ctypes.c_uint32, P, P, P, P, P]),
+        "fp8_experts_zero_rest": (I, [P, I64, I64, ctypes.c_int32, P, P]),
         "fp8_act_grad": (I, [P, P, I64, I64, I, I, P, ctypes.c_uint32, P, P, P, P, P]),
     }
     for name, (res, args) in sig.items():
@@ -278,6 +279,11 @@ def fp8_mm_experts(a8, fa, b8, fb, sa, sb, sb_stride, layout, M, N, K, experts, 
     return _check(lib.fp8_mm_experts(_ptr(a8), fa, _ptr(b8), fb, _ptr(sa), _ptr(sb), sb_stride, layout, M, N, K,
                                      experts, _ptr(offsets), _ptr(bias), act, _ptr(preact), _ptr(out),
                                      _stream(stream)), "fp8_mm_experts")
+
+
+def fp8_experts_zero_rest(out, rows, row_bytes, experts, offsets, stream=None):
+    return _check(lib.fp8_experts_zero_rest(_ptr(out), rows, row_bytes, experts, _ptr(offsets), _stream(stream)),
+                  "fp8_experts_zero_rest")
 
 
 def fp8_act_grad(g, z, rows, cols, act, fmt, ring, flags, out8, amax_out, scale_out, dbias, stream=None):

@@ -499,6 +499,19 @@ expert_kernel(const __grid_constant__ CUtensorMap tm_a, const __grid_constant__ 
     }
 }
 
+// Zeros in the rows of no expert: where the offsets leave none, as they mostly
+// do, the launch reads two offsets and ends (16384 x 4096: 1.1 us where
+// writing all rows takes 34).
+__global__ void zero_rest_kernel(uint4* out, int64_t rows, int64_t pitch, const int32_t* offsets, int experts) {
+    griddep_wait();
+    griddep_launch();
+    const int64_t lo = min(max(int64_t(__ldg(offsets)), int64_t(0)), rows);
+    const int64_t hi = min(max(int64_t(__ldg(offsets + experts)), lo), rows);
+    const int64_t before = lo * pitch, n = before + (rows - hi) * pitch;
+    for (int64_t i = int64_t(blockIdx.x) * blockDim.x + threadIdx.x; i < n; i += int64_t(gridDim.x) * blockDim.x)
+        out[i < before ? i : i - before + hi * pitch] = make_uint4(0u, 0u, 0u, 0u);
+}
+
 template <int BN, int KIND, int STAGES, bool SWAP, int CTAS = 1>
 fp8_status launch_experts(const CUtensorMap& ta, const CUtensorMap& tb, const CUtensorMap& tc, const CUtensorMap& tz,
                           ExpertParams p, int fa, int fb, int64_t most_units, cudaStream_t st) {
@@ -552,6 +565,18 @@ inline bool narrow_sum(int64_t experts, int64_t M, int64_t N) {
 
 }  // namespace
 }  // namespace fp8lite
+
+extern "C" fp8_status fp8_experts_zero_rest(void* out, int64_t rows, int64_t row_bytes, int32_t experts,
+                                            const int32_t* offsets, void* stream) {
+    if (rows < 0 || row_bytes < 1 || experts < 1 || !offsets || (rows > 0 && !out)) return FP8_ERR_INVALID_ARG;
+    if (experts > kMaxExperts || rows >= (int64_t(1) << 31) || row_bytes >= (int64_t(1) << 32)) return FP8_ERR_UNSUPPORTED;
+    if (row_bytes % 16 != 0 || !aligned(out, 16) || !aligned(offsets, 4)) return FP8_ERR_ALIGNMENT;
+    if (rows == 0) return FP8_OK;
+    const int64_t pitch = row_bytes / 16, blocks = (rows * pitch + 255) / 256;
+    const int grid = int(blocks < 4 * int64_t(sm_count()) ? blocks : 4 * int64_t(sm_count()));
+    return launch_pdl(zero_rest_kernel, grid, 256, 0, as_stream(stream), 1, static_cast<uint4*>(out), rows, pitch, offsets,
+                      int(experts));
+}
 
 extern "C" fp8_status fp8_mm_experts(const uint8_t* a8, fp8_fmt fa, const uint8_t* b8, fp8_fmt fb, const float* sa,
                                      const float* sb, int32_t sb_stride, fp8_layout layout, int64_t M, int64_t N,

@@ -15,8 +15,8 @@ all experts and the gradient, kept in `fp8_rings` with the state_dict.
 import torch
 from torch.autograd.function import once_differentiable
 
-from . import (FP8_ACT_NONE, FP8_E4M3, FP8_E5M2, FP8_NN, FP8_NT, FP8_TN, fp8_act_grad_experts, fp8_mm_experts,
-               fp8_ring_init)
+from . import (FP8_ACT_NONE, FP8_E4M3, FP8_E5M2, FP8_NN, FP8_NT, FP8_TN, fp8_act_grad_experts,
+               fp8_experts_zero_rest, fp8_mm_experts, fp8_ring_init)
 from .linear import _RING_WORDS, _act_code, _on_input, _quantize_many, _rows_of
 
 
@@ -35,7 +35,8 @@ class Fp8ExpertsFunction(torch.autograd.Function):
         T, dev = x2.shape[0], x.device
         offsets = offsets.contiguous()
         (x8, sx), (w8, sw) = _quantize_many([(x2, FP8_E4M3, rings[0]), (weight.contiguous(), FP8_E4M3, rings[1])], dev)
-        y = torch.zeros(T, N, dtype=torch.bfloat16, device=dev)  # rows of no expert
+        y = torch.empty(T, N, dtype=torch.bfloat16, device=dev)
+        fp8_experts_zero_rest(y, T, 2 * N, E, offsets)
         z = None
         if act != FP8_ACT_NONE and (ctx.needs_input_grad[0] or any(ctx.needs_input_grad[2:4])):
             z = torch.empty(T, N, dtype=torch.bfloat16, device=dev)
@@ -61,7 +62,8 @@ class Fp8ExpertsFunction(torch.autograd.Function):
         fp8_act_grad_experts(g2, z, T, N, E, offsets, ctx.act, FP8_E5M2, rings[2], 0, g8, stats[0:1], stats[1:2], db)
         sg = stats[1:2]
         if need_x:
-            dx = torch.zeros(T, K, dtype=torch.bfloat16, device=dev)
+            dx = torch.empty(T, K, dtype=torch.bfloat16, device=dev)
+            fp8_experts_zero_rest(dx, T, 2 * K, E, offsets)
             fp8_mm_experts(g8, FP8_E5M2, w8, FP8_E4M3, sg, sw, 0, FP8_NN, T, K, N, E, offsets, None, FP8_ACT_NONE, None, dx)
         if need_w:
             dw = torch.empty(E, N, K, dtype=torch.bfloat16, device=dev)

@@ -464,7 +464,8 @@ FP8LITE_API fp8_status fp8_act_grad(const void* g, const void* z, int64_t rows, 
  *
  * in fp32 with the one rounding of each output, as fp8_mm. Rows before
  * offsets[0] and from offsets[experts] on belong to no expert: NT and NN leave
- * them in out and preact as they are, TN does not read them.
+ * them in out and preact as they are (fp8_experts_zero_rest makes them zeros),
+ * TN's sums do not see them.
  *
  * a8, b8     FP8 codes of formats fa, fb, 16-byte aligned
  * sa         device float: A's scale
@@ -507,6 +508,18 @@ FP8LITE_API fp8_status fp8_act_grad_experts(const void* g, const void* z, int64_
                         int32_t experts, const int32_t* offsets, fp8_act act, fp8_fmt fmt,
                         fp8_ring* ring, uint32_t flags, uint8_t* out8, float* amax_out,
                         float* scale_out, void* dbias, void* stream);
+
+/* Zeros in the rows of `out` that belong to no expert, the ones before
+ * offsets[0] and from offsets[experts] on; the others are left as they are. The
+ * offsets are read on the device, limited to [0, rows].
+ *
+ * out        rows * row_bytes bytes, 16-byte aligned (NULL if rows is 0)
+ * rows       >= 0 and < 2^31; row_bytes: a multiple of 16, < 2^32
+ * experts, offsets   as fp8_mm_experts
+ *
+ * FP8_ERR_INVALID_ARG, FP8_ERR_UNSUPPORTED and FP8_ERR_ALIGNMENT as there. */
+FP8LITE_API fp8_status fp8_experts_zero_rest(void* out, int64_t rows, int64_t row_bytes, int32_t experts,
+                  const int32_t* offsets, void* stream);
 
 /* Workspace bytes fp8_mm_ws needs for this problem and split_k on the
  * current device (split_k 0: for the library's own choice): 0 when that call

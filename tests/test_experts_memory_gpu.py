@@ -81,3 +81,33 @@ def test_after_graphs_and_buffers_are_gone():
         del graph, states, s
         gc.collect()
         torch.cuda.empty_cache()
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("off", [[0, 5, 40], [3, 3, 40], [0, 7, 9], [11, 20, 33], [40, 40, 40], [0, 0, 0], [-5, 3, 99],
+                                 [30, 7, 12]])
+@pytest.mark.parametrize("cols", [8, 2056])
+def test_zeros_in_rows_of_no_expert(off, cols):
+    rows, pad = 40, 64
+    buf = torch.full((rows * cols + 2 * pad,), 7.0, dtype=torch.bfloat16, device="cuda")
+    fp8.fp8_experts_zero_rest(buf[pad:], rows, 2 * cols, 2, torch.tensor(off, dtype=torch.int32, device="cuda"))
+    lo = min(max(off[0], 0), rows)
+    hi = min(max(off[2], lo), rows)
+    v = buf[pad:pad + rows * cols].view(rows, cols)
+    assert (v[:lo] == 0).all() and (v[lo:hi] == 7).all() and (v[hi:] == 0).all()
+    assert (buf[:pad] == 7).all() and (buf[pad + rows * cols:] == 7).all()
+
+
+def test_refusals_of_zeros_in_rows_of_no_expert():
+    A = 0x7F0000000000
+
+    def status(out=A, rows=4, row_bytes=32, experts=2, offsets=A + 64):
+        return fp8.raw_status("fp8_experts_zero_rest", out, rows, row_bytes, experts, offsets, None)
+
+    assert status(rows=0, out=None) == fp8.FP8_OK  # no rows: no launch
+    for bad in (dict(out=None), dict(rows=-1), dict(row_bytes=0), dict(experts=0), dict(offsets=None)):
+        assert status(**bad) == fp8.FP8_ERR_INVALID_ARG, bad
+    for bad in (dict(experts=513), dict(rows=1 << 31), dict(row_bytes=1 << 32)):
+        assert status(**bad) == fp8.FP8_ERR_UNSUPPORTED, bad
+    for bad in (dict(row_bytes=24), dict(out=A + 8), dict(offsets=A + 2)):
+        assert status(**bad) == fp8.FP8_ERR_ALIGNMENT, bad
