@@ -2,6 +2,9 @@
 // fp32, its FP8 codes under a delayed ring, and the bias gradient sum_i dz[i][j].
 //
 // Bound by HBM: 5 bytes an element (g and z in bf16 read, one code written).
+// Measured on B200 with SiLU at 32768 x 4096: 119.7 us, 5.6 TB/s, 0.86 of the
+// measured copy; 2048 x 4096 with GELU tanh (42 MB) 14.0 us, 3.0 TB/s: the launch,
+// the first trip to HBM and the sums' exchange; 37 x 1040 4.2 us, the same alone.
 //
 // Split: a cluster of up to 16 CTAs owns a strip of columns, its CTAs taking
 // row blocks in turn, so that a column's sum is finished inside the cluster:

@@ -6,6 +6,17 @@
 // The product, its tiles and their choice are those of fp8_mm. What the
 // epilogue adds is, per output, the activation's two MUFU instructions and
 // about ten others, 2 bytes of residual read and 2 of preact written.
+//
+// Measured on B200 (graph replay, operands from HBM; the tensor cores' share is
+// of twice the measured bf16 rate, 3256 TF/s):
+//   8192^3 ReLU, bias, residual                375-390 us, 0.87-0.90 of the tensor
+//   2048 x 4096 x 1024 GELU tanh, preact, out8  16.3 us: the last tile's epilogue and
+//                two rounds of tiles (bf16 out without activation 12.2, GELU + 2.1,
+//                preact + 1, codes + 1)
+//   2048 x 1024 x 4096 bias, residual           12.6 us: one round of 32 k-blocks
+//   1001 x 1040 x 2064 NN residual              10.8 us: 72 tiles of 17 k-blocks
+//   1 x 4096 x 4096 SiLU, residual               7.7 us, 2.15 TB/s: launch, one trip
+//                to HBM and the exchange in the cluster
 
 #include "gemm_kernel.cuh"
 

@@ -514,7 +514,8 @@ __device__ __forceinline__ void act_stage(uint32_t stg, const float (&y)[32], in
 // fourth block of 32 columns. Sixteen warps share a tile (four to a TMEM lane
 // quarter and to a scheduler), because the epilogue is bound by latency: a
 // block is a chain of TMEM load, MUFU, staging and store, which one warp a
-// scheduler left bare. Each warp stages and stores its own blocks, so that the
+// scheduler left bare (2048 x 4096 x 1024, GELU to codes with preact: 24.7 us
+// with four warps, 16.3 with sixteen). Each warp stages and stores its own blocks, so that the
 // warps drift apart and overlap; nothing is shared between them, and no
 // barrier holds them together. Per block: z = acc * inv + bias, kept as bf16 if asked
 // for, then act(z) + residual as bf16, or act(z) as FP8 codes under the output
@@ -679,8 +680,9 @@ __device__ __forceinline__ void out8_finish(const GemmParams& p, float m_out, fl
 
 // The epilogue role of an activation launch (unswapped tiles). What a tile
 // needs from global memory is asked for one tile early: its bias (a lane
-// fetches a column of each of its warp's blocks), and its residual as a prefetch into L2, whose first block each warp
-// then loads before the accumulator is there.
+// fetches a column of each of its warp's blocks), and its residual as a
+// prefetch into L2, whose first block each warp then loads before the
+// accumulator is there.
 template <int BN, int CTAS, bool OUT8>
 __device__ __forceinline__ void act_epilogue(const GemmParams& p, const EpArgs<true>& ep, const CUtensorMap* map_c,
                                              float* s_bias, uint32_t stg0, uint32_t tmem_base, uint32_t bar_tfull,
