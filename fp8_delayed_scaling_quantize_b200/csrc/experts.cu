@@ -601,7 +601,7 @@ extern "C" fp8_status fp8_mm_experts(const uint8_t* a8, fp8_fmt fa, const uint8_
     if (!sa || !sb || !offsets || (rows > 0 && !a8) || ((rows > 0 || !sum) && !b8) || ((rows > 0 || sum) && !out))
         return FP8_ERR_INVALID_ARG;
     if (preact && preact == out) return FP8_ERR_INVALID_ARG;
-    if (experts > kMaxExperts || M >= (int64_t(1) << 31) || N >= (int64_t(1) << 31) || K >= (int64_t(1) << 31))
+    if (experts > kMaxExperts || M > kMaxExtent || N > kMaxExtent || K > kMaxExtent)
         return FP8_ERR_UNSUPPORTED;
     if ((sum ? M : K) % 16 != 0 || (layout != FP8_NT && N % 16 != 0)) return FP8_ERR_ALIGNMENT;
     if (!aligned(a8, 16) || !aligned(b8, 16) || !aligned(out, 2) || !aligned(preact, 2) || !aligned(bias, 2))

@@ -51,6 +51,7 @@ fp8_status mm_act_impl(const uint8_t* a8, fp8_fmt fa, const uint8_t* b8, fp8_fmt
     const fp8_status ok = check_mm(a8, fa, b8, fb, sa, sb, layout, M, N, K, batch, stride_a, stride_b, stride_c, bias,
                                    bias_scale, bias_fmt, out, o.out8 ? 1 : 4);
     if (ok != FP8_OK) return ok;
+    if (M > kMaxExtent || N > kMaxExtent || K > kMaxExtent) return FP8_ERR_UNSUPPORTED;
     if (o.residual && (o.stride_r < 0 || (batch > 1 && o.stride_r != 0 && o.stride_r < M * N)))
         return FP8_ERR_INVALID_ARG;
     // out and preact are written as the tiles come: only a residual laid out as out may be out

@@ -390,7 +390,7 @@ typedef enum fp8_act {
  *            one matrix to every batch, else >= M*N when batch > 1
  * preact     NULL, or device bf16[batch*stride_c], laid out as out, 2-byte
  *            aligned, overlapping no other buffer
- * Any M and N that fp8_mm takes; with N and the strides multiples of 8 and
+ * Any M, N and K that fp8_mm takes, up to 2^31 - 1024; with N and the strides multiples of 8 and
  * out, residual and preact 16-byte aligned the outputs leave as whole tiles
  * (faster). Never uses a workspace.
  * Errors: as fp8_mm; FP8_ERR_INVALID_ARG also for a bad act or stride_r, a
@@ -471,7 +471,7 @@ FP8LITE_API fp8_status fp8_act_grad(const void* g, const void* z, int64_t rows, 
  * sa         device float: A's scale
  * sb         device float (sb_stride 0: one scale for all of B) or float[experts]
  *            (sb_stride 1: one for each expert's weight; NT and NN)
- * M, N, K    >= 1, the token rows >= 0, each < 2^31. Multiples of 16: K in NT,
+ * M, N, K    >= 1, the token rows >= 0, each <= 2^31 - 1024. Multiples of 16: K in NT,
  *            K and N in NN, M and N in TN; the token rows and N in NT are free.
  * experts    1 .. FP8_MM_MAX_EXPERTS
  * offsets    device int32[experts + 1], 4-byte aligned, not decreasing, within
@@ -485,8 +485,8 @@ FP8LITE_API fp8_status fp8_act_grad(const void* g, const void* z, int64_t rows, 
  *            buffer. With N a multiple of 8 and out and preact 16-byte
  *            aligned the outputs leave as whole tiles (faster).
  * No workspace. Errors: FP8_ERR_INVALID_ARG (also bias, preact, an activation
- * or sb_stride 1 in TN, and a preact that is out), FP8_ERR_ALIGNMENT, FP8_ERR_UNSUPPORTED (a size >= 2^31
- * or more experts), FP8_ERR_CUDA. A bounded device wait that gives up is
+ * or sb_stride 1 in TN, and a preact that is out), FP8_ERR_ALIGNMENT,
+ * FP8_ERR_UNSUPPORTED (a larger size or more experts), FP8_ERR_CUDA. A bounded device wait that gives up is
  * reported by fp8_last_device_error. */
 #define FP8_MM_MAX_EXPERTS 512
 FP8LITE_API fp8_status fp8_mm_experts(const uint8_t* a8, fp8_fmt fa, const uint8_t* b8, fp8_fmt fb,
