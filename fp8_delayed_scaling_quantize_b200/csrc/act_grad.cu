@@ -28,9 +28,9 @@ namespace {
 
 using namespace sm100;
 
-constexpr int kThreads = 256;
-constexpr int kWarps = kThreads / 32;
-constexpr int kPerSm = 4;  // CTAs of an SM
+constexpr int kThreads = 256;  // of a CTA; tall, narrow tensors take twice as many
+constexpr int kPerSm = 4;      // CTAs of an SM
+constexpr int64_t kTallRows = 8192;  // from here on twice the threads may pay
 constexpr int kMaxRanks = 16;  // CTAs of a cluster (more than 8 by opt-in)
 
 struct GradArgs {
@@ -111,14 +111,15 @@ __device__ __forceinline__ void publish_amax(const GradArgs& a, float* bmax) {
     rr->ticket = 0u;
 }
 
-// W: columns of a strip (64, 32 or 16).
-template <int ACT, int W>
-__global__ void __launch_bounds__(kThreads, kPerSm) act_grad_kernel(const GradArgs a) {
+// W: columns of a strip (64, 32 or 16). THREADS: of a CTA.
+template <int ACT, int W, int THREADS>
+__global__ void __launch_bounds__(THREADS, kPerSm * kThreads / THREADS) act_grad_kernel(const GradArgs a) {
+    constexpr int kWarps = THREADS / 32;
     // rows in flight per thread: with z as many as 64 registers hold; without it
     // twice that (32768 x 4096 without an activation: 79 us with two, 66 with four)
     constexpr int kRows = ACT == FP8_ACT_NONE ? 4 : 2;
     constexpr int kTpr = W / 8;                 // threads of a row
-    constexpr int kBlockRows = kThreads / kTpr;  // rows of a block's pass
+    constexpr int kBlockRows = THREADS / kTpr;  // rows of a block's pass
     __shared__ float part[kWarps][W];
     __shared__ float colsum[W];
     __shared__ uint32_t wmax[kWarps];
@@ -227,14 +228,14 @@ __global__ void __launch_bounds__(kThreads, kPerSm) act_grad_kernel(const GradAr
             for (int w = 0; w < kWarps; ++w) v += part[w][threadIdx.x];
             colsum[threadIdx.x] = v;
         }
-        if (last && threadIdx.x >= kThreads - 32) {
+        if (last && threadIdx.x >= THREADS - 32) {
             const uint32_t bits = __reduce_max_sync(0xffffffffu, lane < kWarps ? wmax[lane] : 0u);
             if (lane == 0) bmax = __uint_as_float(bits);
         }
         if (a.ranks > 1) cluster_sync();
         else             __syncthreads();
         if (rank == 0) {
-            if (last && threadIdx.x == kThreads - 32) publish_amax(a, &bmax);
+            if (last && threadIdx.x == THREADS - 32) publish_amax(a, &bmax);
             if (a.dbias && threadIdx.x < W) {
                 float v = colsum[threadIdx.x];
                 const uint32_t mine = smem_addr(&colsum[threadIdx.x]);
@@ -253,9 +254,9 @@ __global__ void __launch_bounds__(kThreads, kPerSm) act_grad_kernel(const GradAr
     }
 }
 
-template <int ACT, int W>
+template <int ACT, int W, int THREADS>
 fp8_status launch_act(const GradArgs& a, int64_t strips, cudaStream_t st) {
-    auto kern = act_grad_kernel<ACT, W>;
+    auto kern = act_grad_kernel<ACT, W, THREADS>;
     if (a.ranks > 8) {
         static bool allowed[64] = {false};
         int dev = 0;
@@ -266,17 +267,17 @@ fp8_status launch_act(const GradArgs& a, int64_t strips, cudaStream_t st) {
             allowed[dev] = true;
         }
     }
-    return launch_pdl(kern, dim3(unsigned(strips * a.parts * a.ranks)), kThreads, 0, st, a.ranks, a);
+    return launch_pdl(kern, dim3(unsigned(strips * a.parts * a.ranks)), THREADS, 0, st, a.ranks, a);
 }
 
-template <int W>
+template <int W, int THREADS = kThreads>
 fp8_status launch_width(const GradArgs& a, int act, int64_t strips, cudaStream_t st) {
     switch (act) {
-        case FP8_ACT_NONE:      return launch_act<FP8_ACT_NONE, W>(a, strips, st);
-        case FP8_ACT_RELU:      return launch_act<FP8_ACT_RELU, W>(a, strips, st);
-        case FP8_ACT_GELU:      return launch_act<FP8_ACT_GELU, W>(a, strips, st);
-        case FP8_ACT_GELU_TANH: return launch_act<FP8_ACT_GELU_TANH, W>(a, strips, st);
-        default:                return launch_act<FP8_ACT_SILU, W>(a, strips, st);
+        case FP8_ACT_NONE:      return launch_act<FP8_ACT_NONE, W, THREADS>(a, strips, st);
+        case FP8_ACT_RELU:      return launch_act<FP8_ACT_RELU, W, THREADS>(a, strips, st);
+        case FP8_ACT_GELU:      return launch_act<FP8_ACT_GELU, W, THREADS>(a, strips, st);
+        case FP8_ACT_GELU_TANH: return launch_act<FP8_ACT_GELU_TANH, W, THREADS>(a, strips, st);
+        default:                return launch_act<FP8_ACT_SILU, W, THREADS>(a, strips, st);
     }
 }
 
@@ -325,16 +326,26 @@ fp8_status act_grad_impl(const void* g, const void* z, int64_t rows, int64_t col
     // 2048 x 1024 8.8 -> 11.4 and 32768 x 1040 42 -> 51 (fewer of them fit a
     // GPC together).
     const auto strips = [&](int w) { return (cols + w - 1) / w; };
-    const int64_t slots = kPerSm * 148;
-    const int w = strips(64) * experts * 8 >= 2 * 148 ? 64 : strips(32) * experts * 8 >= 2 * 148 ? 32 : 16;
+    // Tall tensors of 296 to 1024 columns, whose clusters of 8 would not fill the
+    // SMs with wider strips, take CTAs of twice the threads instead (us, ReLU /
+    // GELU tanh / none): 65536 x 1024 82 / 78 / 66 -> 58 / 67 / 37, 16384 x 1024
+    // 22.8 / 23.5 / 17.3 -> 19.4 / 22.2 / 14.6, 65536 x 320 45 / 49 / 33 -> 38 /
+    // 39 / 28; at 2048 rows they lost (1024 columns 8.3 / 8.8 / 6.9 -> 8.3 / 9.2 /
+    // 7.3) and past 1024 columns too (4096 x 1040 10.4 -> 12.1: a 33rd cluster).
+    const bool tall = experts == 1 && strips(16) * 8 >= 148 && cols <= 1024 && rows >= kTallRows;
+    const int threads = tall ? 2 * kThreads : kThreads;
+    const int64_t slots = kPerSm * kThreads / threads * 148;
+    const int w = tall ? (strips(32) * 8 >= 148 ? 32 : 16) : strips(64) * experts * 8 >= 2 * 148 ? 64 : strips(32) * experts * 8 >= 2 * 148 ? 32 : 16;
     const int max_ranks = strips(16) * experts * 8 < 148 ? kMaxRanks : 8;
     const int64_t n = strips(w);
     a.parts = int(n * experts <= slots ? experts : slots / n < 1 ? 1 : slots / n);
-    const int64_t block_rows = kThreads / (w / 8);
+    const int64_t block_rows = threads / (w / 8);
     const int64_t blocks = (rows / experts + block_rows - 1) / block_rows;
     a.ranks = 1;
     while (a.ranks < max_ranks && a.ranks < blocks && n * a.parts * a.ranks * 2 <= slots) a.ranks *= 2;
     cudaStream_t st = as_stream(stream);
+    if (tall)
+        return w == 32 ? launch_width<32, 2 * kThreads>(a, act, n, st) : launch_width<16, 2 * kThreads>(a, act, n, st);
     if (w == 64) return launch_width<64>(a, act, n, st);
     if (w == 32) return launch_width<32>(a, act, n, st);
     return launch_width<16>(a, act, n, st);

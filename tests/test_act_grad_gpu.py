@@ -58,6 +58,13 @@ def test_shapes(rows, cols, act):
 
 
 @pytest.mark.gpu
+@pytest.mark.parametrize("rows,cols", [(8191, 296), (8192, 296), (8201, 576), (9999, 584), (10001, 1024), (8192, 1032)])
+@pytest.mark.parametrize("act", [R.NONE, R.RELU, R.GELU, R.GELU_TANH, R.SILU])
+def test_tall_and_narrow(rows, cols, act):
+    test_shapes(rows, cols, act)
+
+
+@pytest.mark.gpu
 def test_no_rows():
     ring = torch.empty(20, dtype=torch.int32, device="cuda")
     fp8.fp8_ring_init(ring, 3.0)
