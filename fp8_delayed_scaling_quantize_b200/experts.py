@@ -16,8 +16,8 @@ import torch
 from torch.autograd.function import once_differentiable
 
 from . import (FP8_ACT_NONE, FP8_E4M3, FP8_E5M2, FP8_NN, FP8_NT, FP8_TN, fp8_act_grad_experts,
-               fp8_experts_zero_rest, fp8_mm_experts, fp8_ring_init)
-from .linear import _RING_WORDS, _act_code, _on_input, _quantize_many, _rows_of
+               fp8_experts_zero_rest, fp8_mm_experts)
+from .linear import Fp8Layer, _act_code, _on_input, _quantize_many, _rows_of
 
 
 class Fp8ExpertsFunction(torch.autograd.Function):
@@ -71,7 +71,7 @@ class Fp8ExpertsFunction(torch.autograd.Function):
         return dx, None, dw, db, None, None
 
 
-class Fp8Experts(torch.nn.Module):
+class Fp8Experts(Fp8Layer):
     """The linears of `experts` experts (bf16 parameters, FP8 compute).
 
     in_features and out_features must be multiples of 16. forward(x, offsets):
@@ -90,19 +90,8 @@ class Fp8Experts(torch.nn.Module):
         kw = {"device": device, "dtype": torch.bfloat16}
         self.weight = torch.nn.Parameter(torch.empty(experts, out_features, in_features, **kw))
         self.bias = torch.nn.Parameter(torch.zeros(experts, out_features, **kw)) if bias else None
-        self.register_buffer("fp8_rings", torch.zeros(3, _RING_WORDS, dtype=torch.int32, device=device))
-        self._rings_ready = False
+        self._make_rings(device)
         torch.nn.init.normal_(self.weight, std=in_features ** -0.5)
-
-    def reset_scaling(self):
-        """Reset the three rings (scale 1, empty history)."""
-        for i in range(3):
-            fp8_ring_init(self.fp8_rings[i], 1.0)
-        self._rings_ready = True
-
-    def _load_from_state_dict(self, *args, **kwargs):
-        super()._load_from_state_dict(*args, **kwargs)
-        self._rings_ready = True  # restored rings are used as they are
 
     def forward(self, x, offsets):
         # the launches go to the current device's stream

@@ -38,10 +38,11 @@ import torch
 from torch.autograd.function import once_differentiable
 
 from . import (FP8_ACT_GELU, FP8_ACT_GELU_TANH, FP8_ACT_NONE, FP8_ACT_RELU, FP8_ACT_SILU, FP8_E4M3, FP8_E5M2, FP8_NN,
-               FP8_NT, FP8_RING_BYTES, FP8_TN, fp8_act_grad, fp8_bias_grad, fp8_mm, fp8_mm_act, fp8_mm_act_out8,
-               fp8_mm_grouped, fp8_quantize, fp8_quantize_many, fp8_ring_init)
+               FP8_NT, FP8_RING_BYTES, FP8_RING_HISTORY, FP8_TN, fp8_act_grad, fp8_bias_grad, fp8_mm, fp8_mm_act,
+               fp8_mm_act_out8, fp8_mm_grouped, fp8_quantize, fp8_quantize_many, fp8_ring_init)
 
 _RING_WORDS = FP8_RING_BYTES // 4
+_SCALE_ONE = 0x3F800000  # the bits of 1.0f
 
 ACTIVATIONS = {None: FP8_ACT_NONE, "relu": FP8_ACT_RELU, "gelu": FP8_ACT_GELU, "gelu_tanh": FP8_ACT_GELU_TANH,
                "silu": FP8_ACT_SILU}
@@ -226,7 +227,43 @@ class Fp8LinearActFunction(torch.autograd.Function):
         return dx, dw, db, None, None, gy if ctx.needs_input_grad[5] else None
 
 
-class Fp8Linear(torch.nn.Module):
+def _fresh_rings(count, device):
+    """`count` rings as fp8_ring_init(ring, 1.0) leaves them."""
+    rings = torch.zeros(count, _RING_WORDS, dtype=torch.int32, device=device)
+    rings[:, FP8_RING_HISTORY] = _SCALE_ONE
+    return rings
+
+
+class Fp8Layer(torch.nn.Module):
+    """A layer with delayed-scaling rings, which are ready for use from the start: the first forward launches no reset,
+    so a graph may capture it."""
+
+    RINGS = 3
+
+    def _make_rings(self, device):
+        self.register_buffer("fp8_rings", _fresh_rings(self.RINGS, device))
+        self._rings_ready = not self.fp8_rings.is_meta  # a layer made without memory resets them in its first forward
+
+    def reset_scaling(self):
+        """Reset the rings (scale 1, empty history)."""
+        for i in range(self.RINGS):
+            fp8_ring_init(self.fp8_rings[i], 1.0)
+        self._rings_ready = True
+
+    def _load_from_state_dict(self, state_dict, prefix, *args, **kwargs):
+        super()._load_from_state_dict(state_dict, prefix, *args, **kwargs)
+        if prefix + "fp8_rings" not in state_dict:
+            return  # weights alone: the rings stay as they are
+        # Restored rings are used as they are, but for those without a scale (a scale of 0 makes every output NaN)
+        with torch.no_grad():
+            scale = self.fp8_rings[:, FP8_RING_HISTORY].contiguous().view(torch.float32)
+            good = (scale > 0) & torch.isfinite(scale)
+            self.fp8_rings.copy_(torch.where(good[:, None], self.fp8_rings,
+                                             _fresh_rings(self.RINGS, self.fp8_rings.device)))
+        self._rings_ready = not self.fp8_rings.is_meta
+
+
+class Fp8Linear(Fp8Layer):
     """Drop-in training linear layer (bf16 parameters, FP8 compute).
 
     in_features and out_features must be multiples of 16 (the GEMMs read
@@ -245,19 +282,8 @@ class Fp8Linear(torch.nn.Module):
         kw = {"device": device, "dtype": torch.bfloat16}
         self.weight = torch.nn.Parameter(torch.empty(out_features, in_features, **kw))
         self.bias = torch.nn.Parameter(torch.zeros(out_features, **kw)) if bias else None
-        self.register_buffer("fp8_rings", torch.zeros(3, _RING_WORDS, dtype=torch.int32, device=device))
-        self._rings_ready = False
+        self._make_rings(device)
         torch.nn.init.normal_(self.weight, std=in_features ** -0.5)
-
-    def reset_scaling(self):
-        """Reset the three rings (scale 1, empty history)."""
-        for i in range(3):
-            fp8_ring_init(self.fp8_rings[i], 1.0)
-        self._rings_ready = True
-
-    def _load_from_state_dict(self, *args, **kwargs):
-        super()._load_from_state_dict(*args, **kwargs)
-        self._rings_ready = True  # restored rings are used as they are
 
     def forward(self, x, residual=None):
         if self._act == FP8_ACT_NONE and residual is None:
@@ -330,7 +356,7 @@ class Fp8MLPFunction(torch.autograd.Function):
         return dx, dw1, db1, dw2, db2, None, None, gy if ctx.needs_input_grad[7] else None
 
 
-class Fp8MLP(torch.nn.Module):
+class Fp8MLP(Fp8Layer):
     """Two FP8 linears with an activation between (bf16 parameters).
 
     features and hidden must be multiples of 16. forward(x, residual) adds a
@@ -350,20 +376,9 @@ class Fp8MLP(torch.nn.Module):
         self.weight2 = torch.nn.Parameter(torch.empty(features, hidden, **kw))
         self.bias1 = torch.nn.Parameter(torch.zeros(hidden, **kw)) if bias else None
         self.bias2 = torch.nn.Parameter(torch.zeros(features, **kw)) if bias else None
-        self.register_buffer("fp8_rings", torch.zeros(self.RINGS, _RING_WORDS, dtype=torch.int32, device=device))
-        self._rings_ready = False
+        self._make_rings(device)
         torch.nn.init.normal_(self.weight1, std=features ** -0.5)
         torch.nn.init.normal_(self.weight2, std=hidden ** -0.5)
-
-    def reset_scaling(self):
-        """Reset the six rings (scale 1, empty history)."""
-        for i in range(self.RINGS):
-            fp8_ring_init(self.fp8_rings[i], 1.0)
-        self._rings_ready = True
-
-    def _load_from_state_dict(self, *args, **kwargs):
-        super()._load_from_state_dict(*args, **kwargs)
-        self._rings_ready = True  # restored rings are used as they are
 
     def forward(self, x, residual=None):
         params = (self.weight1, self.weight2, self.bias1, self.bias2, residual)
