@@ -17,7 +17,7 @@ from torch.autograd.function import once_differentiable
 
 from . import (FP8_ACT_NONE, FP8_E4M3, FP8_E5M2, FP8_NN, FP8_NT, FP8_TN, fp8_act_grad_experts,
                fp8_experts_zero_rest, fp8_mm_experts)
-from .linear import Fp8Layer, _act_code, _on_input, _quantize_many, _rows_of
+from .linear import Fp8Layer, _act_code, _dense, _on_input, _quantize_many, _rows_of
 
 
 class Fp8ExpertsFunction(torch.autograd.Function):
@@ -34,7 +34,7 @@ class Fp8ExpertsFunction(torch.autograd.Function):
             raise ValueError(f"offsets must be int32 [{E + 1}] on the input's device")
         T, dev = x2.shape[0], x.device
         offsets = offsets.contiguous()
-        (x8, sx), (w8, sw) = _quantize_many([(x2, FP8_E4M3, rings[0]), (weight.contiguous(), FP8_E4M3, rings[1])], dev)
+        (x8, sx), (w8, sw) = _quantize_many([(x2, FP8_E4M3, rings[0]), (_dense(weight), FP8_E4M3, rings[1])], dev)
         y = torch.empty(T, N, dtype=torch.bfloat16, device=dev)
         fp8_experts_zero_rest(y, T, 2 * N, E, offsets)
         z = None
@@ -54,7 +54,7 @@ class Fp8ExpertsFunction(torch.autograd.Function):
         need_x, need_w, need_b = ctx.needs_input_grad[0], ctx.needs_input_grad[2], ctx.needs_input_grad[3]
         dx = dw = db = None
         dev = gy.device
-        g2 = gy.to(torch.bfloat16).contiguous()
+        g2 = _dense(gy.to(torch.bfloat16))
         g8 = torch.empty(T * N, dtype=torch.uint8, device=dev)
         stats = torch.empty(2, dtype=torch.float32, device=dev)
         if need_b and ctx.has_bias:

@@ -54,13 +54,19 @@ def _act_code(activation):
     return ACTIVATIONS[activation]
 
 
+def _dense(t):
+    """t contiguous and from a 16-byte boundary on, as the kernels load it: a view that starts elsewhere is copied."""
+    t = t.contiguous()
+    return t if t.data_ptr() % 16 == 0 else t.clone()
+
+
 def _rows_of(x, features, what):
-    """x as contiguous rows [T, features]."""
+    """x as dense rows [T, features]."""
     if x.shape[-1] != features:
         raise ValueError(f"{what} features {x.shape[-1]} != {features}")
     if x.dtype != torch.bfloat16:
         raise TypeError(f"{what} must be bf16")
-    return x.reshape(-1, features).contiguous()
+    return _dense(x.reshape(-1, features))
 
 
 def _on_input(x, rings, *params):
@@ -93,8 +99,8 @@ class Fp8LinearFunction(torch.autograd.Function):
             raise ValueError(f"input features {x.shape[-1]} != weight's {K}")
         if x.dtype != torch.bfloat16 or weight.dtype != torch.bfloat16:
             raise TypeError("Fp8Linear takes bf16 inputs and weights")
-        x2 = x.reshape(-1, K).contiguous()
-        w = weight.contiguous()
+        x2 = _dense(x.reshape(-1, K))
+        w = _dense(weight)
         T = x2.shape[0]
         # x and W in one quantize launch (each with its own ring)
         dev = x.device
@@ -118,7 +124,7 @@ class Fp8LinearFunction(torch.autograd.Function):
         x8, w8, sx, sw, rings = ctx.saved_tensors
         T, N, K = ctx.dims
         need_x, need_w, need_b = ctx.needs_input_grad[0], ctx.needs_input_grad[1], ctx.needs_input_grad[2]
-        g2 = gy.reshape(-1, N).to(torch.bfloat16).contiguous()
+        g2 = _dense(gy.reshape(-1, N).to(torch.bfloat16))
         dx = dw = db = None
         if need_x or need_w:
             g8, sg = _quantize(g2, T * N, FP8_E5M2, rings[2])
@@ -194,7 +200,7 @@ class Fp8LinearActFunction(torch.autograd.Function):
                 raise ValueError(f"residual shape {tuple(residual.shape)} != {(*x.shape[:-1], N)}")
             r2 = _rows_of(residual, N, "residual")
         dev = x.device
-        (x8, sx), (w8, sw) = _quantize_many([(x2, FP8_E4M3, rings[0]), (weight.contiguous(), FP8_E4M3, rings[1])], dev)
+        (x8, sx), (w8, sw) = _quantize_many([(x2, FP8_E4M3, rings[0]), (_dense(weight), FP8_E4M3, rings[1])], dev)
         y = torch.empty(T, N, dtype=torch.bfloat16, device=dev)
         z = None
         if act != FP8_ACT_NONE and any(ctx.needs_input_grad[:3]):
@@ -215,7 +221,7 @@ class Fp8LinearActFunction(torch.autograd.Function):
         need_b = need_b and ctx.has_bias
         dx = dw = db = None
         if need_x or need_w or need_b:
-            g2 = gy.reshape(-1, N).to(torch.bfloat16).contiguous()
+            g2 = _dense(gy.reshape(-1, N).to(torch.bfloat16))
             g8, sg, db = _grad_codes(g2, z, ctx.act, rings[2], need_b)
             if T:
                 dx, dw = _dx_dw(g8, sg, w8, sw, x8, sx, T, N, K, need_x, need_w)
@@ -316,7 +322,7 @@ class Fp8MLPFunction(torch.autograd.Function):
             r2 = _rows_of(residual, N, "residual")
         b1, b2 = (b.contiguous() if b is not None else None for b in (b1, b2))
         (x8, sx), (w18, sw1), (w28, sw2) = _quantize_many(
-            [(x2, FP8_E4M3, rings[0]), (w1.contiguous(), FP8_E4M3, rings[1]), (w2.contiguous(), FP8_E4M3, rings[3])], dev)
+            [(x2, FP8_E4M3, rings[0]), (_dense(w1), FP8_E4M3, rings[1]), (_dense(w2), FP8_E4M3, rings[3])], dev)
         z = torch.empty(T, H, dtype=torch.bfloat16, device=dev) if any(ctx.needs_input_grad[:5]) else None
         h8 = torch.empty(T * H, dtype=torch.uint8, device=dev)
         stats = torch.empty(2, dtype=torch.float32, device=dev)
@@ -340,7 +346,7 @@ class Fp8MLPFunction(torch.autograd.Function):
         dx = dw1 = db1 = dw2 = db2 = None
         inner = need_x or need_w1 or need_b1
         if T and (inner or need_w2 or need_b2):
-            g2 = gy.reshape(-1, N).to(torch.bfloat16).contiguous()
+            g2 = _dense(gy.reshape(-1, N).to(torch.bfloat16))
             g8, sg, db2 = _grad_codes(g2, None, FP8_ACT_NONE, rings[4], need_b2)
             dh, dw2 = _dx_dw(g8, sg, w28, sw2, h8, sh, T, N, H, inner, need_w2)
             if inner:
