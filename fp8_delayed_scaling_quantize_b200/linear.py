@@ -305,8 +305,9 @@ class Fp8Linear(Fp8Layer):
 
 class Fp8MLPFunction(torch.autograd.Function):
     """y = act(x W1^T + b1) W2^T + b2 + residual. The hidden activation goes
-    from the first product to the second as E4M3 codes under its own ring; the
-    backward pass keeps its input z in bf16. Rings: x, W1, hidden, W2, the
+    from the first product to the second as E4M3 codes under its own ring; for
+    the backward pass its input z is kept in bf16, where the activation's
+    gradient is asked for. Rings: x, W1, hidden, W2, the
     gradients of the output and of z."""
 
     @staticmethod
@@ -323,7 +324,9 @@ class Fp8MLPFunction(torch.autograd.Function):
         b1, b2 = (b.contiguous() if b is not None else None for b in (b1, b2))
         (x8, sx), (w18, sw1), (w28, sw2) = _quantize_many(
             [(x2, FP8_E4M3, rings[0]), (_dense(w1), FP8_E4M3, rings[1]), (_dense(w2), FP8_E4M3, rings[3])], dev)
-        z = torch.empty(T, H, dtype=torch.bfloat16, device=dev) if any(ctx.needs_input_grad[:5]) else None
+        z = None
+        if act != FP8_ACT_NONE and any(ctx.needs_input_grad[:3]):  # what the first product's gradients read
+            z = torch.empty(T, H, dtype=torch.bfloat16, device=dev)
         h8 = torch.empty(T * H, dtype=torch.uint8, device=dev)
         stats = torch.empty(2, dtype=torch.float32, device=dev)
         sh = stats[1:2]
