@@ -25,7 +25,7 @@ class Fp8ExpertsFunction(torch.autograd.Function):
     expert give zeros and get zero gradients."""
 
     @staticmethod
-    def forward(ctx, x, offsets, weight, bias, rings, act):
+    def forward(ctx, x, offsets, weight, bias, rings, act, learn=True):
         E, N, K = weight.shape
         x2 = _rows_of(x, K, "input")
         if x.dim() != 2:
@@ -38,7 +38,7 @@ class Fp8ExpertsFunction(torch.autograd.Function):
         y = torch.empty(T, N, dtype=torch.bfloat16, device=dev)
         fp8_experts_zero_rest(y, T, 2 * N, E, offsets)
         z = None
-        if act != FP8_ACT_NONE and (ctx.needs_input_grad[0] or any(ctx.needs_input_grad[2:4])):
+        if act != FP8_ACT_NONE and learn and (ctx.needs_input_grad[0] or any(ctx.needs_input_grad[2:4])):
             z = torch.empty(T, N, dtype=torch.bfloat16, device=dev)
         b = bias.contiguous() if bias is not None else None
         fp8_mm_experts(x8, FP8_E4M3, w8, FP8_E4M3, sx, sw, 0, FP8_NT, T, N, K, E, offsets, b, act, z, y)
@@ -68,7 +68,7 @@ class Fp8ExpertsFunction(torch.autograd.Function):
         if need_w:
             dw = torch.empty(E, N, K, dtype=torch.bfloat16, device=dev)
             fp8_mm_experts(g8, FP8_E5M2, x8, FP8_E4M3, sg, sx, 0, FP8_TN, N, K, T, E, offsets, None, FP8_ACT_NONE, None, dw)
-        return dx, None, dw, db, None, None
+        return dx, None, dw, db, None, None, None
 
 
 class Fp8Experts(Fp8Layer):
@@ -98,4 +98,5 @@ class Fp8Experts(Fp8Layer):
         with torch.cuda.device(_on_input(x, self.fp8_rings, self.weight, self.bias)):
             if not self._rings_ready:
                 self.reset_scaling()
-            return Fp8ExpertsFunction.apply(x, offsets, self.weight, self.bias, self.fp8_rings, self._act)
+            return Fp8ExpertsFunction.apply(x, offsets, self.weight, self.bias, self.fp8_rings, self._act,
+                                            torch.is_grad_enabled())

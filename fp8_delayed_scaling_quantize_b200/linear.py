@@ -185,10 +185,13 @@ def _dx_dw(g8, sg, w8, sw, x8, sx, T, N, K, need_x, need_w):
 
 
 class Fp8LinearActFunction(torch.autograd.Function):
-    """y = act(x W^T + b) + residual with FP8 operands and delayed scaling."""
+    """y = act(x W^T + b) + residual with FP8 operands and delayed scaling.
+    learn: whether gradients are recorded, which a Function cannot see for
+    itself (under no_grad its needs_input_grad are those of the leaves); without
+    them the activation's input is not kept."""
 
     @staticmethod
-    def forward(ctx, x, weight, bias, rings, act, residual):
+    def forward(ctx, x, weight, bias, rings, act, residual, learn=True):
         N, K = weight.shape
         x2 = _rows_of(x, K, "input")
         T = x2.shape[0]
@@ -203,7 +206,7 @@ class Fp8LinearActFunction(torch.autograd.Function):
         (x8, sx), (w8, sw) = _quantize_many([(x2, FP8_E4M3, rings[0]), (_dense(weight), FP8_E4M3, rings[1])], dev)
         y = torch.empty(T, N, dtype=torch.bfloat16, device=dev)
         z = None
-        if act != FP8_ACT_NONE and any(ctx.needs_input_grad[:3]):
+        if act != FP8_ACT_NONE and learn and any(ctx.needs_input_grad[:3]):
             z = torch.empty(T, N, dtype=torch.bfloat16, device=dev)
         b = bias.contiguous() if bias is not None else None
         if T:
@@ -230,7 +233,7 @@ class Fp8LinearActFunction(torch.autograd.Function):
                 dw = torch.zeros(N, K, dtype=torch.bfloat16, device=gy.device) if need_w else None
             if need_x:
                 dx = dx.reshape(ctx.x_shape)
-        return dx, dw, db, None, None, gy if ctx.needs_input_grad[5] else None
+        return dx, dw, db, None, None, gy if ctx.needs_input_grad[5] else None, None
 
 
 def _fresh_rings(count, device):
@@ -300,7 +303,8 @@ class Fp8Linear(Fp8Layer):
         with torch.cuda.device(_on_input(x, self.fp8_rings, self.weight, self.bias, residual)):
             if not self._rings_ready:
                 self.reset_scaling()
-            return Fp8LinearActFunction.apply(x, self.weight, self.bias, self.fp8_rings, self._act, residual)
+            return Fp8LinearActFunction.apply(x, self.weight, self.bias, self.fp8_rings, self._act, residual,
+                                              torch.is_grad_enabled())
 
 
 class Fp8MLPFunction(torch.autograd.Function):
@@ -311,7 +315,7 @@ class Fp8MLPFunction(torch.autograd.Function):
     gradients of the output and of z."""
 
     @staticmethod
-    def forward(ctx, x, w1, b1, w2, b2, rings, act, residual):
+    def forward(ctx, x, w1, b1, w2, b2, rings, act, residual, learn=True):
         H, D = w1.shape
         N = w2.shape[0]
         x2 = _rows_of(x, D, "input")
@@ -325,7 +329,7 @@ class Fp8MLPFunction(torch.autograd.Function):
         (x8, sx), (w18, sw1), (w28, sw2) = _quantize_many(
             [(x2, FP8_E4M3, rings[0]), (_dense(w1), FP8_E4M3, rings[1]), (_dense(w2), FP8_E4M3, rings[3])], dev)
         z = None
-        if act != FP8_ACT_NONE and any(ctx.needs_input_grad[:3]):  # what the first product's gradients read
+        if act != FP8_ACT_NONE and learn and any(ctx.needs_input_grad[:3]):  # what the first product's gradients read
             z = torch.empty(T, H, dtype=torch.bfloat16, device=dev)
         h8 = torch.empty(T * H, dtype=torch.uint8, device=dev)
         stats = torch.empty(2, dtype=torch.float32, device=dev)
@@ -362,7 +366,7 @@ class Fp8MLPFunction(torch.autograd.Function):
             dx = zero(*ctx.x_shape) if need_x else None
             dw1, db1 = zero(H, D) if need_w1 else None, zero(H) if need_b1 else None
             dw2, db2 = zero(N, H) if need_w2 else None, zero(N) if need_b2 else None
-        return dx, dw1, db1, dw2, db2, None, None, gy if ctx.needs_input_grad[7] else None
+        return dx, dw1, db1, dw2, db2, None, None, gy if ctx.needs_input_grad[7] else None, None
 
 
 class Fp8MLP(Fp8Layer):
@@ -395,4 +399,4 @@ class Fp8MLP(Fp8Layer):
             if not self._rings_ready:
                 self.reset_scaling()
             return Fp8MLPFunction.apply(x, self.weight1, self.bias1, self.weight2, self.bias2, self.fp8_rings, self._act,
-                                        residual)
+                                        residual, torch.is_grad_enabled())

@@ -3,7 +3,7 @@
 import pytest
 import torch
 
-from fp8_delayed_scaling_quantize_b200 import linear
+from fp8_delayed_scaling_quantize_b200 import experts, linear
 
 pytestmark = pytest.mark.gpu
 
@@ -49,3 +49,20 @@ def test_mlp(monkeypatch, activation, learn):
     for name, p, q in [("x", xs, xw), *((n, p, dict(whole.named_parameters())[n]) for n, p in mlp.named_parameters())]:
         assert (p.grad is not None) == (name in LEARN[learn])
         assert p.grad is None or torch.equal(p.grad, q.grad), name
+
+
+def test_without_gradients_nothing_is_kept(monkeypatch):
+    x = torch.randn(20, 64, device="cuda").bfloat16().requires_grad_(True)
+    off = torch.tensor([0, 9, 20], dtype=torch.int32, device="cuda")
+    kept = [_spy(monkeypatch, linear, "fp8_mm_act_out8", 18), _spy(monkeypatch, linear, "fp8_mm_act", 20),
+            _spy(monkeypatch, experts, "fp8_mm_experts", 15)]
+    layers = [(linear.Fp8MLP(64, 128, device="cuda"), ()), (linear.Fp8Linear(64, 64, device="cuda", activation="gelu"), ()),
+              (experts.Fp8Experts(2, 64, 64, device="cuda", activation="gelu"), (off,))]
+    for layer, more in layers:
+        with torch.no_grad():
+            y = layer(x, *more)
+        assert y.grad_fn is None
+    assert kept == [[False], [False, False], [False]]
+    for layer, more in layers:
+        layer(x, *more)
+    assert kept == [[False, True], [False, False, False, True], [False, True]]
