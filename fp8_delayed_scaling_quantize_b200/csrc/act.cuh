@@ -117,12 +117,18 @@ __device__ __forceinline__ F2 act_fwd(F2 z) {
 template <int ACT>
 __device__ __forceinline__ F2 act_slope(uint32_t zz) {
     if (ACT == FP8_ACT_NONE) return f2(1.0f);
+    if (ACT == FP8_ACT_RELU) {
+        // s = z > 0 on the pair, and min(max(z, s), s): s again, but NaN where z is
+        // (32768 x 4096: 105.4 us; 105.0 where a NaN gives 0, 107.6 by compares in fp32)
+        uint32_t s;
+        asm("set.gt.bf16x2.bf16x2 %0, %1, %2;" : "=r"(s) : "r"(zz), "r"(0u));
+        asm("max.NaN.bf16x2 %0, %0, %1;\n\tmin.NaN.bf16x2 %0, %0, %1;" : "+r"(zz) : "r"(s));
+        return f2(__uint_as_float(zz << 16), __uint_as_float(zz & 0xFFFF0000u));
+    }
     // bf16 pairs: 100; -10 (GELU tanh), -87 (SiLU), -100 (GELU)
     constexpr uint32_t kLo = ACT == FP8_ACT_GELU_TANH ? 0xC120C120u : ACT == FP8_ACT_SILU ? 0xC2AEC2AEu : 0xC2C8C2C8u;
-    if (ACT != FP8_ACT_RELU)
-        asm("max.NaN.bf16x2 %0, %0, %1;\n\tmin.NaN.bf16x2 %0, %0, %2;" : "+r"(zz) : "r"(kLo), "r"(0x42C842C8u));
+    asm("max.NaN.bf16x2 %0, %0, %1;\n\tmin.NaN.bf16x2 %0, %0, %2;" : "+r"(zz) : "r"(kLo), "r"(0x42C842C8u));
     const float z0 = __uint_as_float(zz << 16), z1 = __uint_as_float(zz & 0xFFFF0000u);
-    if (ACT == FP8_ACT_RELU) return f2(z0 > 0.0f ? 1.0f : 0.0f, z1 > 0.0f ? 1.0f : 0.0f);
     const F2 z = f2(z0, z1);
     if (ACT == FP8_ACT_GELU) {
         F2 e;

@@ -359,8 +359,8 @@ FP8LITE_API fp8_status fp8_mm_out8(const uint8_t* a8, fp8_fmt fa, const uint8_t*
  *   GELU       z Phi(z), Phi the normal distribution function (erf)
  *   GELU_TANH  z (1 + tanh(sqrt(2/pi) (z + 0.044715 z^3))) / 2
  *   SILU       z / (1 + exp(-z))
- * A NaN stays NaN; at -inf and +inf the activations give their limits, 0 and
- * +inf, and their slopes 0 and 1. */
+ * A NaN stays NaN, in the activations and in their slopes; at -inf and +inf the
+ * activations give their limits, 0 and +inf, and their slopes 0 and 1. */
 typedef enum fp8_act {
     FP8_ACT_NONE = 0,
     FP8_ACT_RELU = 1,
