@@ -1,17 +1,25 @@
 // The activations of the GEMM epilogues and of the activation gradient, in
 // fp32. sigmoid(x) = 1 / (1 + 2^(-x log2 e)) takes the two MUFU instructions
 // ex2.approx and rcp.approx, whose documented errors are 2 ulp and 1 ulp: the
-// results are within a few 2^-23 of the formula (relative to z), far below
-// the bf16 or FP8 rounding that follows. Their .ftz forms are one instruction
-// each, where the others scale subnormals around it; only results below
-// 2^-126 are flushed. Everything else runs on pairs (fma.rn.f32x2 and its
+// results are within a few 2^-23 of the formula (relative to z; for GELU's
+// tail see below), under the bf16 or FP8 rounding that follows. Their .ftz forms are one instruction
+// each, where the others scale subnormals around it; only a sigmoid or an
+// exponential below 2^-126 is flushed. Everything else runs on pairs (fma.rn.f32x2 and its
 // like), which rounds each half as the scalar instruction would at half the
 // instructions: the epilogues and the gradient are bound by issue before they
 // are by MUFU.
 //   ReLU       z < 0 ? 0 : z                       (NaN stays NaN)
-//   GELU       z Phi(z), Phi(z) = (1 + erf(z / sqrt 2)) / 2, erf by the
-//              rational form 7.1.26 of Abramowitz and Stegun's handbook
-//              (absolute error 1.5e-7)
+//   GELU       z Phi(z), Phi(z) = (1 + erf(z / sqrt 2)) / 2 = 1 - Phi(-z), and
+//              for x >= 0 Phi(-x) = exp(-x^2 / 2) P(1 / (1 + c x)), the form of
+//              7.1.26 in Abramowitz and Stegun's handbook. That formula's own P,
+//              of degree 5, is good to 7.5e-8 absolutely, which is 0.4 % of
+//              Phi(-5) and 1 % of Phi(-8). The slope Phi(z) + z phi(z) takes it:
+//              there z phi(z) outweighs Phi by z^2, and the tail is off by
+//              less than 3e-4 of itself. The activation takes a P of degree 6, fitted
+//              here to the smaller of 6e-8 absolute and 1e-4 relative error
+//              over x <= 14.5, so that the tail too keeps the precision of its
+//              rounding (in the slope it would cost 3 %: 32768 x 4096 147.4 ->
+//              152.0 us; in the product 1 %: 2048 x 4096 x 1024 16.1 -> 16.3)
 //   GELU tanh  z (1 + tanh u) / 2 = z sigmoid(2 u),
 //              u = sqrt(2 / pi) (z + 0.044715 z^3)
 //   SiLU       z sigmoid(z)
@@ -78,14 +86,25 @@ constexpr float kGeluT0 = -2.3022081985f;
 constexpr float kGeluT1 = -0.1029432396f;
 
 // Phi(z), the standard normal distribution function; e is exp(-z^2 / 2).
+// TAIL: to a relative 1e-4 however small.
+template <bool TAIL>
 __device__ __forceinline__ F2 normal_cdf(F2 z, F2& e) {
-    const F2 t = rcp2(fma2(z & 0x7FFFFFFF7FFFFFFFull, f2(0.23164189f), f2(1.0f)));  // 0.3275911 / sqrt 2
+    // c; for 7.1.26 0.3275911 / sqrt 2, and half of its a1 t + ... + a5 t^5 below
+    const F2 t = rcp2(fma2(z & 0x7FFFFFFF7FFFFFFFull, f2(TAIL ? 0.292f : 0.23164189f), f2(1.0f)));
     e = ex2_2(mul2(mul2(z, z), f2(-0.5f * kLog2e)));
-    // half of (a1 t + a2 t^2 + a3 t^3 + a4 t^4 + a5 t^5)
-    F2 p = fma2(t, f2(0.5307027145f), f2(-0.7265760135f));
-    p = fma2(t, p, f2(0.7107068705f));
-    p = fma2(t, p, f2(-0.142248368f));
-    p = fma2(t, p, f2(0.127414796f));
+    F2 p;
+    if (TAIL) {
+        p = fma2(t, f2(-0.08670647f), f2(0.2705679f));
+        p = fma2(t, p, f2(-0.07591453f));
+        p = fma2(t, p, f2(0.17060119f));
+        p = fma2(t, p, f2(0.10403046f));
+        p = fma2(t, p, f2(0.11742138f));
+    } else {
+        p = fma2(t, f2(0.5307027145f), f2(-0.7265760135f));
+        p = fma2(t, p, f2(0.7107068705f));
+        p = fma2(t, p, f2(-0.142248368f));
+        p = fma2(t, p, f2(0.127414796f));
+    }
     const F2 q = mul2(mul2(t, p), e);
     float z0, z1, q0, q1, r0, r1;
     split(z, z0, z1);
@@ -105,7 +124,7 @@ __device__ __forceinline__ F2 act_fwd(F2 z) {
     z = f2(at_least(a, -100.0f), at_least(b, -100.0f));
     if (ACT == FP8_ACT_GELU) {
         F2 e;
-        return mul2(z, normal_cdf(z, e));
+        return mul2(z, normal_cdf<true>(z, e));
     }
     const F2 x = ACT == FP8_ACT_GELU_TANH ? mul2(z, fma2(mul2(z, z), f2(kGeluT1), f2(kGeluT0))) : mul2(z, f2(-kLog2e));
     return mul2(z, rcp2(add2(ex2_2(x), f2(1.0f))));
@@ -132,7 +151,7 @@ __device__ __forceinline__ F2 act_slope(uint32_t zz) {
     const F2 z = f2(z0, z1);
     if (ACT == FP8_ACT_GELU) {
         F2 e;
-        const F2 c = normal_cdf(z, e);
+        const F2 c = normal_cdf<false>(z, e);
         return fma2(z, mul2(e, f2(0.3989422804f)), c);  // Phi + z phi
     }
     // y = z s: y' = s + s z (1 - s) w', where s = 1 / (1 + e) and 1 - s = e s (no cancellation)
