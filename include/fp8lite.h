@@ -500,8 +500,8 @@ FP8LITE_API fp8_status fp8_mm_experts(const uint8_t* a8, fp8_fmt fa, const uint8
  * for one without rows). One ring and one scale for all. Rows of no expert
  * count for nothing and keep what their out8 holds.
  * experts    1 .. FP8_MM_MAX_EXPERTS
- * offsets    device int32[experts + 1] as fp8_mm_experts'; others are limited
- *            to [0, rows] and to the expert's first
+ * offsets    device int32[experts + 1] as fp8_mm_experts', others limited in
+ *            the same way
  * Other arguments and errors as fp8_act_grad; FP8_ERR_INVALID_ARG also for a
  * NULL offsets or experts < 1, FP8_ERR_UNSUPPORTED for more experts. */
 FP8LITE_API fp8_status fp8_act_grad_experts(const void* g, const void* z, int64_t rows, int64_t cols,
@@ -511,7 +511,8 @@ FP8LITE_API fp8_status fp8_act_grad_experts(const void* g, const void* z, int64_
 
 /* Zeros in the rows of `out` that belong to no expert, the ones before
  * offsets[0] and from offsets[experts] on; the others are left as they are. The
- * offsets are read on the device, limited to [0, rows].
+ * offsets are read on the device, and others than fp8_mm_experts' limited in the
+ * same way: exactly the rows that NT and NN leave become zeros.
  *
  * out        rows * row_bytes bytes, 16-byte aligned (NULL if rows is 0)
  * rows       >= 0 and < 2^31; row_bytes: a multiple of 16, < 2^32
