@@ -31,7 +31,8 @@ using namespace sm100;
 constexpr int kThreads = 256;  // of a CTA; tall, narrow tensors take twice as many
 constexpr int kPerSm = 4;      // CTAs of an SM
 constexpr int64_t kTallRows = 8192;  // from here on twice the threads may pay
-constexpr int kMaxRanks = 16;  // CTAs of a cluster (more than 8 by opt-in)
+constexpr int kPortableRanks = 8;  // CTAs of a cluster that every device holds
+constexpr int kMaxRanks = 16;      // by opt-in, where the device holds them
 
 struct GradArgs {
     const uint4* g;
@@ -274,18 +275,37 @@ __global__ void __launch_bounds__(THREADS, kPerSm * kThreads / THREADS) act_grad
     }
 }
 
+// Clusters of `cluster` CTAs that the current device holds at a time: 0 if none
+// of its GPCs has the SMs for one.
+int max_clusters(void (*kern)(GradArgs), int threads, int cluster) {
+    cudaLaunchAttribute attr = {};
+    attr.id = cudaLaunchAttributeClusterDimension;
+    attr.val.clusterDim.x = unsigned(cluster);
+    attr.val.clusterDim.y = attr.val.clusterDim.z = 1;
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = dim3(unsigned(cluster));
+    cfg.blockDim = dim3(unsigned(threads));
+    cfg.attrs = &attr;
+    cfg.numAttrs = 1;
+    int n = 0;
+    if (cudaOccupancyMaxActiveClusters(&n, kern, &cfg) == cudaSuccess) return n;
+    cudaGetLastError();  // clears it
+    return 0;
+}
+
 template <int ACT, int W, int THREADS, bool EXPERTS>
-fp8_status launch_kernel(const GradArgs& a, int64_t strips, cudaStream_t st) {
+fp8_status launch_kernel(GradArgs a, int64_t strips, cudaStream_t st) {
     auto kern = act_grad_kernel<ACT, W, THREADS, EXPERTS>;
-    if (a.ranks > 8) {
-        static bool allowed[64] = {false};
+    if (a.ranks > kPortableRanks) {
+        static int fits[64] = {0};  // 1: the device holds such a cluster, -1: it does not
         int dev = 0;
         if (cudaGetDevice(&dev) != cudaSuccess || dev < 0 || dev >= 64) return FP8_ERR_CUDA;
-        if (!allowed[dev]) {
+        if (fits[dev] == 0) {
             if (cudaFuncSetAttribute(kern, cudaFuncAttributeNonPortableClusterSizeAllowed, 1) != cudaSuccess)
                 return FP8_ERR_CUDA;
-            allowed[dev] = true;
+            fits[dev] = max_clusters(kern, THREADS, kMaxRanks) > 0 ? 1 : -1;
         }
+        if (fits[dev] < 0) a.ranks = kPortableRanks;
     }
     return launch_pdl(kern, dim3(unsigned(strips * a.parts * a.ranks)), THREADS, 0, st, a.ranks, a);
 }
@@ -351,6 +371,7 @@ fp8_status act_grad_impl(const void* g, const void* z, int64_t rows, int64_t col
     // measured on B200 (SiLU, us, 8 against 16) 32768 x 128 20.9 -> 14.3, but
     // 2048 x 1024 8.8 -> 11.4 and 32768 x 1040 42 -> 51 (fewer of them fit a
     // GPC together).
+    const int64_t sms = sm_count();
     const auto strips = [&](int w) { return (cols + w - 1) / w; };
     // Tall tensors of 296 to 1024 columns, whose clusters of 8 would not fill the
     // SMs with wider strips, take CTAs of twice the threads instead (us, ReLU /
@@ -358,11 +379,14 @@ fp8_status act_grad_impl(const void* g, const void* z, int64_t rows, int64_t col
     // 22.8 / 23.5 / 17.3 -> 19.4 / 22.2 / 14.6, 65536 x 320 45 / 49 / 33 -> 38 /
     // 39 / 28; at 2048 rows they lost (1024 columns 8.3 / 8.8 / 6.9 -> 8.3 / 9.2 /
     // 7.3) and past 1024 columns too (4096 x 1040 10.4 -> 12.1: a 33rd cluster).
-    const bool tall = experts == 1 && strips(16) * 8 >= 148 && cols <= 1024 && rows >= kTallRows;
+    const bool tall = experts == 1 && strips(16) * 8 >= sms && cols <= 1024 && rows >= kTallRows;
     const int threads = tall ? 2 * kThreads : kThreads;
-    const int64_t slots = kPerSm * kThreads / threads * 148;
-    const int w = tall ? (strips(32) * 8 >= 148 ? 32 : 16) : strips(64) * experts * 8 >= 2 * 148 ? 64 : strips(32) * experts * 8 >= 2 * 148 ? 32 : 16;
-    const int max_ranks = strips(16) * experts * 8 < 148 ? kMaxRanks : 8;
+    const int64_t slots = kPerSm * kThreads / threads * sms;
+    const int w = tall                                  ? (strips(32) * 8 >= sms ? 32 : 16)
+                  : strips(64) * experts * 8 >= 2 * sms ? 64
+                  : strips(32) * experts * 8 >= 2 * sms ? 32
+                                                        : 16;
+    const int max_ranks = strips(16) * experts * 8 < sms ? kMaxRanks : kPortableRanks;
     const int64_t n = strips(w);
     a.parts = int(n * experts <= slots ? experts : slots / n < 1 ? 1 : slots / n);
     const int64_t block_rows = threads / (w / 8);

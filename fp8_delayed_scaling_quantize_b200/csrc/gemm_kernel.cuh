@@ -1537,18 +1537,6 @@ bool make_out8_map(CUtensorMap* map, void* base, uint64_t n, uint64_t m, uint64_
            CUDA_SUCCESS;
 }
 
-int sm_count() {
-    static int cached[64] = {0};
-    int dev = 0;
-    if (cudaGetDevice(&dev) != cudaSuccess || dev < 0 || dev >= 64) return 148;
-    if (cached[dev] == 0) {
-        int c = 0;
-        if (cudaDeviceGetAttribute(&c, cudaDevAttrMultiProcessorCount, dev) != cudaSuccess || c <= 0) c = 148;
-        cached[dev] = c;
-    }
-    return cached[dev];
-}
-
 struct HostArgs {
     int fa, fb;
     const void* b8;

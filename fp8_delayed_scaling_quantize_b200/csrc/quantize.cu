@@ -568,18 +568,6 @@ __global__ void rings_fold_kernel(fp8_ring* rings, int count, const __grid_const
     griddep_launch();
 }
 
-int sm_count() {
-    static int cached[64] = {0};
-    int dev = 0;
-    if (cudaGetDevice(&dev) != cudaSuccess || dev < 0 || dev >= 64) return 148;
-    if (cached[dev] == 0) {
-        int c = 0;
-        if (cudaDeviceGetAttribute(&c, cudaDevAttrMultiProcessorCount, dev) != cudaSuccess || c <= 0) c = 148;
-        cached[dev] = c;
-    }
-    return cached[dev];
-}
-
 // Blocks of a single-tensor launch. Every block adds its amax and takes a
 // ticket on the ring's one cache line, and those same-address atomics queue
 // (about 2 ns each on B200), so below 64 M elements the grid is kept at one
