@@ -295,14 +295,12 @@ class Fp8Linear(Fp8Layer):
         torch.nn.init.normal_(self.weight, std=in_features ** -0.5)
 
     def forward(self, x, residual=None):
-        if self._act == FP8_ACT_NONE and residual is None:
-            if not self._rings_ready:
-                self.reset_scaling()
-            return Fp8LinearFunction.apply(x, self.weight, self.bias, self.fp8_rings)
         # the launches go to the current device's stream
         with torch.cuda.device(_on_input(x, self.fp8_rings, self.weight, self.bias, residual)):
             if not self._rings_ready:
                 self.reset_scaling()
+            if self._act == FP8_ACT_NONE and residual is None:
+                return Fp8LinearFunction.apply(x, self.weight, self.bias, self.fp8_rings)
             return Fp8LinearActFunction.apply(x, self.weight, self.bias, self.fp8_rings, self._act, residual,
                                               torch.is_grad_enabled())
 
