@@ -15,7 +15,7 @@ all experts and the gradient, kept in `fp8_rings` with the state_dict.
 import torch
 from torch.autograd.function import once_differentiable
 
-from . import (FP8_ACT_NONE, FP8_E4M3, FP8_E5M2, FP8_NN, FP8_NT, FP8_TN, fp8_act_grad_experts,
+from . import (FP8_ACT_NONE, FP8_E4M3, FP8_E5M2, FP8_MM_MAX_EXPERTS, FP8_NN, FP8_NT, FP8_TN, fp8_act_grad_experts,
                fp8_experts_zero_rest, fp8_mm_experts)
 from .linear import Fp8Layer, _act_code, _dense, _on_input, _quantize_many, _rows_of
 
@@ -74,7 +74,8 @@ class Fp8ExpertsFunction(torch.autograd.Function):
 class Fp8Experts(Fp8Layer):
     """The linears of `experts` experts (bf16 parameters, FP8 compute).
 
-    in_features and out_features must be multiples of 16. forward(x, offsets):
+    in_features and out_features must be multiples of 16, experts at most
+    FP8_MM_MAX_EXPERTS (512). forward(x, offsets):
     x bf16 [T, in_features] sorted by expert, offsets int32 [experts + 1] on the
     same device. activation as Fp8Linear's. Rows of no expert give zeros; their
     input values still count for the input's scale.
@@ -84,6 +85,8 @@ class Fp8Experts(Fp8Layer):
         super().__init__()
         if in_features % 16 or out_features % 16:
             raise ValueError("Fp8Experts needs in_features and out_features divisible by 16")
+        if not 1 <= experts <= FP8_MM_MAX_EXPERTS:
+            raise ValueError(f"Fp8Experts takes 1 to {FP8_MM_MAX_EXPERTS} experts, not {experts}")
         self.experts, self.in_features, self.out_features = experts, in_features, out_features
         self.activation = activation
         self._act = _act_code(activation)
