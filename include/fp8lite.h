@@ -407,7 +407,11 @@ FP8LITE_API fp8_status fp8_mm_act(const uint8_t* a8, fp8_fmt fa, const uint8_t* 
 /* fp8_mm_act whose output is the FP8 operand of the next product, as
  * fp8_mm_out8's: out8[b,i,j] = sat_rne_out_fmt( fp32(act(z[b,i,j]) * s) ) with
  * s = out_ring->scale as it stood before the call, and the amax of |act(z)|
- * folded into out_ring. preact as fp8_mm_act; there is no residual.
+ * folded into out_ring. The fold is not deferred, as fp8_mm_out8's is not: a
+ * ring of either call cannot join a data-parallel exchange of the amaxes, and
+ * replicas' scales for these outputs follow their own. preact as fp8_mm_act;
+ * there is no residual. Never swaps operands: few rows take longer than
+ * fp8_mm_act's (1 x 4096 x 4096 15 us against 8).
  * Errors: as fp8_mm_out8; FP8_ERR_INVALID_ARG also for a bad act and for a
  * preact that is out8. */
 FP8LITE_API fp8_status fp8_mm_act_out8(const uint8_t* a8, fp8_fmt fa, const uint8_t* b8, fp8_fmt fb,
