@@ -97,9 +97,8 @@ class Fp8Experts(Fp8Layer):
         torch.nn.init.normal_(self.weight, std=in_features ** -0.5)
 
     def forward(self, x, offsets):
-        # the launches go to the current device's stream
-        with torch.cuda.device(_on_input(x, self.fp8_rings, self.weight, self.bias)):
+        rings, weight, bias = self.fp8_rings, self.weight, self.bias
+        with _on_input(x, rings, weight, bias):
             if not self._rings_ready:
                 self.reset_scaling()
-            return Fp8ExpertsFunction.apply(x, offsets, self.weight, self.bias, self.fp8_rings, self._act,
-                                            torch.is_grad_enabled())
+            return Fp8ExpertsFunction.apply(x, offsets, weight, bias, rings, self._act, torch.is_grad_enabled())

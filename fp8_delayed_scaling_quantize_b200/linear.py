@@ -34,6 +34,8 @@ time (an output that was kept, say): its leaves are bound to the eager stream,
 and torch would make that stream wait for the capture.
 """
 
+import contextlib
+
 import torch
 from torch.autograd.function import once_differentiable
 
@@ -69,16 +71,24 @@ def _rows_of(x, features, what):
     return _dense(x.reshape(-1, features))
 
 
+_HERE = contextlib.nullcontext()
+_current_device = getattr(torch._C, "_cuda_getDevice", torch.cuda.current_device)
+
+
 def _on_input(x, rings, *params):
-    """What the kernels take by address: bf16 parameters and the rings on the input's GPU. Returns that device."""
+    """What the kernels take by address: bf16 parameters and the rings on the input's GPU. Returns a context in which
+    that GPU is current: the launches go to the current device's stream."""
     for t in params:
-        if t is not None and t.dtype != torch.bfloat16:
+        if t is not None and t.dtype is not torch.bfloat16:
             raise TypeError("parameters and residual must be bf16")
-    if not x.is_cuda:
+    dev = x.get_device()
+    if dev < 0:
         raise ValueError("the input must be on a GPU")
-    if any(t is not None and t.device != x.device for t in (rings, *params)):
-        raise ValueError(f"parameters and rings must be on the input's device {x.device}")
-    return x.device
+    for t in (rings, *params):
+        if t is not None and t.get_device() != dev:
+            raise ValueError(f"parameters and rings must be on the input's device {x.device}")
+    # a device context costs 3 us, asking for the current device a tenth of that
+    return _HERE if dev == _current_device() else torch.cuda.device(dev)
 
 
 def _quantize(t, n, fmt, ring):
@@ -295,14 +305,13 @@ class Fp8Linear(Fp8Layer):
         torch.nn.init.normal_(self.weight, std=in_features ** -0.5)
 
     def forward(self, x, residual=None):
-        # the launches go to the current device's stream
-        with torch.cuda.device(_on_input(x, self.fp8_rings, self.weight, self.bias, residual)):
+        rings, weight, bias = self.fp8_rings, self.weight, self.bias
+        with _on_input(x, rings, weight, bias, residual):
             if not self._rings_ready:
                 self.reset_scaling()
             if self._act == FP8_ACT_NONE and residual is None:
-                return Fp8LinearFunction.apply(x, self.weight, self.bias, self.fp8_rings)
-            return Fp8LinearActFunction.apply(x, self.weight, self.bias, self.fp8_rings, self._act, residual,
-                                              torch.is_grad_enabled())
+                return Fp8LinearFunction.apply(x, weight, bias, rings)
+            return Fp8LinearActFunction.apply(x, weight, bias, rings, self._act, residual, torch.is_grad_enabled())
 
 
 class Fp8MLPFunction(torch.autograd.Function):
@@ -392,9 +401,8 @@ class Fp8MLP(Fp8Layer):
         torch.nn.init.normal_(self.weight2, std=hidden ** -0.5)
 
     def forward(self, x, residual=None):
-        params = (self.weight1, self.weight2, self.bias1, self.bias2, residual)
-        with torch.cuda.device(_on_input(x, self.fp8_rings, *params)):  # the launches go to the current device's stream
+        rings, params = self.fp8_rings, (self.weight1, self.bias1, self.weight2, self.bias2)
+        with _on_input(x, rings, *params, residual):
             if not self._rings_ready:
                 self.reset_scaling()
-            return Fp8MLPFunction.apply(x, self.weight1, self.bias1, self.weight2, self.bias2, self.fp8_rings, self._act,
-                                        residual, torch.is_grad_enabled())
+            return Fp8MLPFunction.apply(x, *params, rings, self._act, residual, torch.is_grad_enabled())
