@@ -1,25 +1,26 @@
 // The activations of the GEMM epilogues and of the activation gradient, in
 // fp32. sigmoid(x) = 1 / (1 + 2^(-x log2 e)) takes the two MUFU instructions
 // ex2.approx and rcp.approx, whose documented errors are 2 ulp and 1 ulp: the
-// results are within a few 2^-23 of the formula (relative to z; for GELU's
-// tail see below), under the bf16 or FP8 rounding that follows. Their .ftz forms are one instruction
-// each, where the others scale subnormals around it; only a sigmoid or an
-// exponential below 2^-126 is flushed. Everything else runs on pairs (fma.rn.f32x2 and its
-// like), which rounds each half as the scalar instruction would at half the
-// instructions: the epilogues and the gradient are bound by issue before they
-// are by MUFU.
+// results are within a few 2^-23 of the formula (relative to z; GELU's tail is
+// below), under the bf16 or FP8 rounding that follows. Their .ftz forms are one
+// instruction each, where the others scale subnormals around it; only a sigmoid
+// or an exponential below 2^-126 is flushed. Everything else runs on pairs
+// (fma.rn.f32x2 and its like), which rounds each half as the scalar instruction
+// would at half the instructions: the epilogues and the gradient are bound by
+// issue before they are by MUFU.
 //   ReLU       z < 0 ? 0 : z                       (NaN stays NaN)
 //   GELU       z Phi(z), Phi(z) = (1 + erf(z / sqrt 2)) / 2 = 1 - Phi(-z), and
 //              for x >= 0 Phi(-x) = exp(-x^2 / 2) P(1 / (1 + c x)), the form of
-//              7.1.26 in Abramowitz and Stegun's handbook. That formula's own P,
-//              of degree 5, is good to 7.5e-8 absolutely, which is 0.4 % of
-//              Phi(-5) and 1 % of Phi(-8). The slope Phi(z) + z phi(z) takes it:
-//              there z phi(z) outweighs Phi by z^2, and the tail is off by
-//              less than 3e-4 of itself. The activation takes a P of degree 6, fitted
-//              here to the smaller of 6e-8 absolute and 1e-4 relative error
-//              over x <= 14.5, so that the tail too keeps the precision of its
-//              rounding (in the slope it would cost 3 %: 32768 x 4096 147.4 ->
-//              152.0 us; in the product 1 %: 2048 x 4096 x 1024 16.1 -> 16.3)
+//              7.1.26 in Abramowitz and Stegun's handbook. That formula's own
+//              P, of degree 5, is good to 7.5e-8 absolutely, which is 0.4 % of
+//              Phi(-5) and 1 % of Phi(-8). The slope Phi(z) + z phi(z) takes
+//              it: there z phi(z) outweighs Phi by z^2, and the tail is off by
+//              less than 3e-4 of itself. The activation takes a P of degree 6,
+//              fitted here to the smaller of 6e-8 absolute and 1e-4 relative
+//              error over x <= 14.5, so that the tail too keeps the precision
+//              of its rounding (in the slope it would cost 3 %: 32768 x 4096
+//              147.4 -> 152.0 us; in the product 1 %: 2048 x 4096 x 1024
+//              16.1 -> 16.3)
 //   GELU tanh  z (1 + tanh u) / 2 = z sigmoid(2 u),
 //              u = sqrt(2 / pi) (z + 0.044715 z^3)
 //   SiLU       z sigmoid(z)
